@@ -56,7 +56,9 @@ typedef enum {
 
 typedef enum {
     ALSPEC_F32 = 0,   /* IEEE binary32                       */
-    ALSPEC_BF16 = 1   /* bfloat16 (upper half of a binary32) */
+    ALSPEC_BF16 = 1,  /* bfloat16 (upper half of a binary32) */
+    ALSPEC_E4M3 = 2   /* 8-bit float, 4 exponent bits, largest value 448, no infinity;
+                         pages of alspec_paged_cache only */
 } alspec_dtype;
 
 /* Compute engine of the attention kernels (alspec_desc.engine). */
@@ -120,6 +122,9 @@ typedef enum {
  * index outside its buffer (shared-memory slot, chunk list, partial slot,
  * copy source or output) and skipped that access; outputs invalid. */
 #define ALSPEC_DEVERR_BOUNDS 0x4u
+/* The paged entry points: a page table entry outside [0, n_pages), or a
+ * sequence number or position of alspec_paged_append outside the table. */
+#define ALSPEC_DEVERR_PAGE 0x8u
 
 /*
  * Problem description.  Shapes (row-major, last index fastest):
@@ -427,6 +432,177 @@ alspec_status alspec_decode_noalloc(const alspec_desc* desc,
  * ALSPEC_ERR_INVALID_ARG for a NULL err.  Allocates nothing.
  */
 alspec_status alspec_noalloc_device_error(void* stream, uint32_t* err);
+
+/* ------------------------------------------------------------ paged cache
+ *
+ * A key-value cache kept in pages of page_size tokens, for batches whose
+ * sequences grow and end at different times.  Sequence b's token t lives in
+ * row t % page_size of page page_table[b][t / page_size]; pages may be
+ * shared between sequences (for reading) and lie in any order.
+ *
+ * Row (page, KV head, slot) of k_pages and v_pages starts at element
+ *   page * page_stride + head * head_stride + slot * token_stride
+ * and holds head_dim consecutive elements; the strides are those of both
+ * pools.  All three strides 0 stand for the contiguous layout
+ * [n_pages][n_kv_heads][page_size][head_dim]; token-major pages
+ * ([n_pages][page_size][n_kv_heads][head_dim]) have head_stride = head_dim
+ * and token_stride = n_kv_heads * head_dim.
+ *
+ * ALSPEC_E4M3 pages hold codes; value = code * scale with one fp32 scale per
+ * (page, KV head, slot), in k_scales and v_scales, contiguous
+ * [n_pages][n_kv_heads][page_size].
+ *
+ * Supported: head_dim 64 or 128; page_size a positive multiple of 8;
+ * k_pages and v_pages 16-byte aligned; strides of at least head_dim
+ * elements whose byte counts are multiples of 16 (and below 2^40).
+ * The scale pointers are read for ALSPEC_E4M3 only.
+ */
+typedef struct {
+    void* k_pages;        /* device */
+    void* v_pages;        /* device */
+    float* k_scales;      /* device, ALSPEC_E4M3 only */
+    float* v_scales;      /* device, ALSPEC_E4M3 only */
+    int64_t page_stride;  /* elements; 0, 0, 0 = contiguous */
+    int64_t head_stride;
+    int64_t token_stride;
+    int n_pages;
+    int page_size;
+    int n_kv_heads;
+    int head_dim;
+    int dtype;            /* alspec_dtype: ALSPEC_F32, ALSPEC_BF16 or ALSPEC_E4M3 */
+    int reserved;         /* 0 */
+} alspec_paged_cache;
+
+/*
+ * Write new tokens' keys and values into their pages.
+ *   k, v        device, src_dtype (ALSPEC_F32 or ALSPEC_BF16): token i's row of
+ *               n_kv_heads * head_dim elements starts at i * k_stride
+ *               (v_stride) elements; a stride of 0 stands for
+ *               n_kv_heads * head_dim.  16-byte aligned, strides whose byte
+ *               counts are multiples of 16 (slices of one fused projection's
+ *               rows are fine).
+ *   positions   device int32 [n_tokens]: token i becomes token positions[i]
+ *               of its sequence; a negative position marks padding, and that
+ *               token is not written.
+ *   seq_ids     device int32 [n_tokens]: token i's sequence (row of
+ *               page_table), or NULL: token i is sequence i's (a decode step;
+ *               n_tokens <= batch).
+ *   page_table  device int32 [batch][max_pages]
+ *   err         device uint32 or NULL: ALSPEC_DEVERR_* bits are ORed in.  A
+ *               token whose sequence, position or page is out of range is
+ *               not written and sets ALSPEC_DEVERR_PAGE.
+ * Conversion: fp32 and bf16 pages hold the value rounded to nearest even.
+ * e4m3 pages: for each (token, KV head) row, scale = max(amax / 448, 2^-126)
+ * with amax the row's largest magnitude, code = the e4m3 value nearest to
+ * x / scale (ties to even), every step in fp32.  A row that holds a NaN or an
+ * infinity reads back as NaN.  A row named twice in one call ends up with
+ * one of the values given for each of its elements, not necessarily of the
+ * same token.  n_tokens 0 is a no-op.  Rows that no token names keep their
+ * contents.  Asynchronous on `stream`, one launch.
+ */
+alspec_status alspec_paged_append(const alspec_paged_cache* cache, const void* k, const void* v,
+                                  int src_dtype, int64_t k_stride, int64_t v_stride,
+                                  const int32_t* positions, const int32_t* seq_ids, int n_tokens,
+                                  const int32_t* page_table, int batch, int max_pages,
+                                  uint32_t* err, void* stream);
+
+/*
+ * Read pages back into one contiguous cache (the layout alspec_decode takes):
+ *   k_out, v_out  device, out_dtype (ALSPEC_F32 or ALSPEC_BF16)
+ *                 [batch][n_kv_heads][max_seq_len][head_dim], 16-byte aligned
+ *   seq_lens      device int32 [batch], 0 <= L_b <= min(max_seq_len,
+ *                 max_pages * page_size): rows [0, L_b) of sequence b are
+ *                 written (values, rounded once to out_dtype), rows from L_b
+ *                 on keep their contents.  A length out of range is clamped
+ *                 and sets ALSPEC_DEVERR_SEQ_LEN.
+ *   err           device uint32 or NULL.  Rows of a page out of range are not
+ *                 written and set ALSPEC_DEVERR_PAGE.
+ * Asynchronous on `stream`, one launch.
+ */
+alspec_status alspec_paged_gather(const alspec_paged_cache* cache, const int32_t* page_table,
+                                  int max_pages, const int32_t* seq_lens, int batch,
+                                  int max_seq_len, int out_dtype, void* k_out, void* v_out,
+                                  uint32_t* err, void* stream);
+
+/*
+ * Bytes of device workspace alspec_paged_decode needs on the current device;
+ * the same for every batch and length.  Zero it once with
+ * alspec_workspace_init.  Returns 0 if the cache description, the batch or
+ * n_q_heads is invalid or unsupported (the pointers are not looked at).
+ */
+size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, int n_q_heads);
+
+/*
+ * Softmax attention of one new token per sequence over its pages:
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t
+ * over the tokens t in [0, L_b), or, with n_sink + window > 0, over the sink
+ * set [0, n_sink) u [L_b - window, L_b) alone (a set union, each token once).
+ * Query head h reads KV head h / (n_q_heads / n_kv_heads).
+ *   q           device [batch][n_q_heads][head_dim], fp32 for ALSPEC_F32 pages
+ *               and bf16 otherwise, 16-byte aligned; sequence b's row starts
+ *               at b * q_stride elements (0: contiguous), whose byte count is
+ *               a multiple of 16
+ *   page_table  device int32 [batch][max_pages]; entries behind a sequence's
+ *               last page are not read.  An entry outside [0, n_pages) sets
+ *               ALSPEC_DEVERR_PAGE and that sequence's output is undefined.
+ *   seq_lens    device int32 [batch], 0 <= L_b <= max_pages * page_size; out
+ *               of range: clamped, ALSPEC_DEVERR_SEQ_LEN.  A sequence of
+ *               length 0 (a padded row of the batch) gets zeros, and -inf in
+ *               lse.
+ *   n_sink, window  both 0: the whole cache
+ *   scale       softmax scale, finite; 0 stands for 1/sqrt(head_dim)
+ *   out         device [batch][n_q_heads][head_dim], out_dtype (ALSPEC_F32 or
+ *               ALSPEC_BF16), 16-byte aligned
+ *   lse         device fp32 [batch][n_q_heads] or NULL: the natural logarithm
+ *               of sum_t exp(scale * q . k_t), for joining the output with
+ *               attention over other tokens
+ *   workspace   device, alspec_paged_workspace_size() bytes, zeroed once by
+ *               alspec_workspace_init; one call at a time per workspace (calls
+ *               ordered on one stream, and graphs replayed one after another,
+ *               may share one).  alspec_get_device_error reads its error word.
+ *   timeout_ms  bound on any in-kernel wait; 0 = 2000
+ * Rows behind L_b in the last page may hold anything, NaN included.  Sums and
+ * softmax statistics are fp32; results do not depend on timing (no float
+ * atomics).  Any group size n_q_heads / n_kv_heads; batch <= 65535.
+ * Asynchronous on `stream`, one launch, no allocation; safe to capture.
+ */
+alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q, int64_t q_stride,
+                                  int n_q_heads, const int32_t* page_table, int max_pages,
+                                  const int32_t* seq_lens, int batch, int n_sink, int window,
+                                  float scale, int out_dtype, void* out, float* lse,
+                                  int timeout_ms, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Activation of alspec_linear. */
+typedef enum {
+    ALSPEC_ACT_NONE = 0,
+    ALSPEC_ACT_RELU = 1,  /* max(x, 0); NaN stays NaN       */
+    ALSPEC_ACT_GELU = 2,  /* x (1 + erf(x / sqrt 2)) / 2    */
+    ALSPEC_ACT_SILU = 3   /* x / (1 + exp(-x))              */
+} alspec_activation;
+
+/*
+ * Linear layer of a decode batch, on the tensor cores, with its epilogue:
+ *     y[r][j] = activation(sum_i x[r][i] w[j][i] + bias[j]) + residual[r][j]
+ * (alspec_oproj is the form for fp32 activations of up to 8 rows.)
+ *   x         device bf16 [rows][k], row r at r * x_stride elements (0: k;
+ *             a multiple of 8, at least k), 16-byte aligned
+ *   w         device bf16 [n][k] contiguous, 16-byte aligned
+ *   bias      device bf16 [n], or NULL
+ *   residual  device [rows][n] contiguous in y's type, or NULL; it may be y
+ *             itself
+ *   y         device [rows][n] contiguous, out_dtype ALSPEC_F32 or ALSPEC_BF16,
+ *             aligned to its element; must not overlap x or w
+ *   err       device uint32 or NULL: ALSPEC_DEVERR_TIMEOUT is ORed in when one
+ *             of the kernel's bounded waits (2 s) expires (y is then
+ *             incomplete)
+ * Sums, bias, activation and residual are fp32; y is rounded once.  rows >= 0
+ * (0: a no-op), n >= 1, k a positive multiple of 8.  Asynchronous on
+ * `stream`, one launch, no workspace.
+ */
+alspec_status alspec_linear(const void* x, int64_t x_stride, const void* w, const void* bias,
+                            const void* residual, void* y, int out_dtype, int activation,
+                            int rows, int n, int k, uint32_t* err, void* stream);
 
 #ifdef __cplusplus
 }

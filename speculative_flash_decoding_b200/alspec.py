@@ -34,16 +34,19 @@ ALSPEC_ERR_DEVICE_DATA = 6
 
 ALSPEC_F32 = 0
 ALSPEC_BF16 = 1
+ALSPEC_E4M3 = 2   # pages of alspec_paged_cache only
 
 ALSPEC_PROF_EVENTS = 5
 
 ALSPEC_DEVERR_SEQ_LEN = 0x1
 ALSPEC_DEVERR_TIMEOUT = 0x2
 ALSPEC_DEVERR_BOUNDS = 0x4   # bounds-checked debug build only
+ALSPEC_DEVERR_PAGE = 0x8     # page table entry, sequence or position out of range
 
 # Every symbol the header declares, with (restype, argtypes).
 _vp, _i, _f, _sz, _u32p = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
                           ctypes.POINTER(ctypes.c_uint32))
+_i64 = ctypes.c_int64
 
 
 ALSPEC_ENGINE_AUTO = 0
@@ -62,7 +65,15 @@ class alspec_desc(ctypes.Structure):
                 ("engine", _i), ("schedule", _i)]
 
 
+class alspec_paged_cache(ctypes.Structure):
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_scales", _vp), ("v_scales", _vp),
+                ("page_stride", _i64), ("head_stride", _i64), ("token_stride", _i64),
+                ("n_pages", _i), ("page_size", _i), ("n_kv_heads", _i), ("head_dim", _i),
+                ("dtype", _i), ("reserved", _i)]
+
+
 _descp = ctypes.POINTER(alspec_desc)
+_pagedp = ctypes.POINTER(alspec_paged_cache)
 
 SIGNATURES = {
     "alspec_workspace_size": (_sz, [_descp, _i, _i]),
@@ -90,6 +101,13 @@ SIGNATURES = {
     "alspec_test_wait_timeout": (_i, [_vp, _sz, _i, _vp]),
     "alspec_decode_oproj": (_i, [_descp, _vp, _vp, _vp, _vp, _i, _i, _f, _vp, _i, _vp, _vp,
                                  _vp, _vp, _vp, _i, _vp, _sz, _vp, _vp]),
+    "alspec_paged_append": (_i, [_pagedp, _vp, _vp, _i, _i64, _i64, _vp, _vp, _i, _vp, _i, _i,
+                                 _vp, _vp]),
+    "alspec_paged_gather": (_i, [_pagedp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "alspec_paged_workspace_size": (_sz, [_pagedp, _i, _i]),
+    "alspec_paged_decode": (_i, [_pagedp, _vp, _i64, _i, _vp, _i, _vp, _i, _i, _i, _f, _i, _vp,
+                                 _vp, _i, _vp, _sz, _vp]),
+    "alspec_linear": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
 }
 
 ALSPEC_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -219,6 +237,51 @@ def alspec_query_chunks(desc: alspec_desc, n_sink: int, window: int):
     st = int(_lib.alspec_query_chunks(ctypes.byref(desc), n_sink, window, fq, cap,
                                       ctypes.byref(n2), ctypes.byref(tile)))
     return st, list(fq)[: n2.value + 1], tile.value
+
+
+ALSPEC_ACT_NONE, ALSPEC_ACT_RELU, ALSPEC_ACT_GELU, ALSPEC_ACT_SILU = 0, 1, 2, 3
+ACTIVATIONS = {"none": ALSPEC_ACT_NONE, "relu": ALSPEC_ACT_RELU, "gelu": ALSPEC_ACT_GELU,
+               "silu": ALSPEC_ACT_SILU}
+
+
+def alspec_paged_append(cache: alspec_paged_cache, k: int, v: int, src_dtype: int, k_stride: int,
+                        v_stride: int, positions: int, seq_ids: int, n_tokens: int,
+                        page_table: int, batch: int, max_pages: int, err: int,
+                        stream: int) -> int:
+    """Write n_tokens new rows of K and V into their pages."""
+    return _lib.alspec_paged_append(cache, k, v, src_dtype, k_stride, v_stride, positions,
+                                    seq_ids, n_tokens, page_table, batch, max_pages, err, stream)
+
+
+def alspec_paged_gather(cache: alspec_paged_cache, page_table: int, max_pages: int,
+                        seq_lens: int, batch: int, max_seq_len: int, out_dtype: int, k_out: int,
+                        v_out: int, err: int, stream: int) -> int:
+    """Read pages back into contiguous K and V caches."""
+    return _lib.alspec_paged_gather(cache, page_table, max_pages, seq_lens, batch, max_seq_len,
+                                    out_dtype, k_out, v_out, err, stream)
+
+
+def alspec_paged_workspace_size(cache: alspec_paged_cache, batch: int, n_q_heads: int) -> int:
+    return int(_lib.alspec_paged_workspace_size(cache, batch, n_q_heads))
+
+
+def alspec_paged_decode(cache: alspec_paged_cache, q: int, q_stride: int, n_q_heads: int,
+                        page_table: int, max_pages: int, seq_lens: int, batch: int, n_sink: int,
+                        window: int, scale: float, out_dtype: int, out: int, lse: int,
+                        timeout_ms: int, workspace: int, workspace_bytes: int,
+                        stream: int) -> int:
+    """Softmax attention of one new token per sequence over its pages."""
+    return _lib.alspec_paged_decode(cache, q, q_stride, n_q_heads, page_table, max_pages,
+                                    seq_lens, batch, n_sink, window, scale, out_dtype, out, lse,
+                                    timeout_ms, workspace, workspace_bytes, stream)
+
+
+def alspec_linear(x: int, x_stride: int, w: int, bias: int, residual: int, y: int,
+                  out_dtype: int, activation: int, rows: int, n: int, k: int, err: int,
+                  stream: int) -> int:
+    """y = activation(x W^T + bias) + residual."""
+    return _lib.alspec_linear(x, x_stride, w, bias, residual, y, out_dtype, activation, rows, n,
+                              k, err, stream)
 
 
 def alspec_get_device_error(workspace: int, workspace_bytes: int, stream: int):

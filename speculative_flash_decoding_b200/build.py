@@ -20,14 +20,16 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libalspec.so")
 DEBUG_LIB = os.path.join(PKG, "libalspec_debug.so")
 PROBE_LIB = os.path.join(PKG, "libalspec_read_probe.so")
-_DECODE_DEPS = ([os.path.join(CSRC, f) for f in ("attn_kernels.cuh", "oproj_kernels.cuh",
-                                                 "ptx.cuh")] +
+_DECODE_SRCS = [os.path.join(CSRC, f) for f in ("alspec.cu", "linear.cu", "paged.cu")]
+_DECODE_DEPS = ([os.path.join(CSRC, f) for f in ("attn_kernels.cuh", "common.cuh", "host.h",
+                                                 "linear_kernels.cuh", "oproj_kernels.cuh",
+                                                 "paged_kernels.cuh", "ptx.cuh")] +
                 [os.path.join(INCLUDE, "alspec.h")])
-# (library, its source, the headers it depends on, extra nvcc flags)
+# (library, its sources, the headers they depend on, extra nvcc flags)
 TARGETS = [
-    (LIB, os.path.join(CSRC, "alspec.cu"), _DECODE_DEPS, []),
-    (DEBUG_LIB, os.path.join(CSRC, "alspec.cu"), _DECODE_DEPS, ["-DALSPEC_DEBUG_BOUNDS"]),
-    (PROBE_LIB, os.path.join(CSRC, "read_probe.cu"),
+    (LIB, _DECODE_SRCS, _DECODE_DEPS, []),
+    (DEBUG_LIB, _DECODE_SRCS, _DECODE_DEPS, ["-DALSPEC_DEBUG_BOUNDS"]),
+    (PROBE_LIB, [os.path.join(CSRC, "read_probe.cu")],
      [os.path.join(CSRC, "ptx.cuh"), os.path.join(INCLUDE, "alspec_read_probe.h")], []),
 ]
 
@@ -35,6 +37,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-shared", "-Xcompiler", "-fPIC", "-cudart", "static",
+    "-t", "0",  # the sources of a library side by side
 ]
 
 
@@ -45,13 +48,13 @@ def nvcc() -> str:
     return "nvcc"
 
 
-def _build_one(lib: str, src: str, deps, flags, force: bool, verbose: bool) -> None:
+def _build_one(lib: str, srcs, deps, flags, force: bool, verbose: bool) -> None:
     if not force and os.path.exists(lib):
-        newest = max(os.path.getmtime(p) for p in [src, *deps])
+        newest = max(os.path.getmtime(p) for p in [*srcs, *deps])
         if os.path.getmtime(lib) >= newest:
             return
     tmp = lib + ".tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, *flags, "-I", INCLUDE, "-I", CSRC, "-o", tmp, src]
+    cmd = [nvcc(), *NVCC_FLAGS, *flags, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *srcs]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)
@@ -60,8 +63,8 @@ def _build_one(lib: str, src: str, deps, flags, force: bool, verbose: bool) -> N
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every library of the package; return the decode library's path."""
-    for lib, src, deps, flags in TARGETS:
-        _build_one(lib, src, deps, flags, force, verbose)
+    for lib, srcs, deps, flags in TARGETS:
+        _build_one(lib, srcs, deps, flags, force, verbose)
     return LIB
 
 

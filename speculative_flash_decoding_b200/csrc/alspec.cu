@@ -19,12 +19,12 @@
 
 #include "alspec.h"
 #include "attn_kernels.cuh"
+#include "host.h"
 #include "oproj_kernels.cuh"
 
 namespace alspec {
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kMaxSpecItems = kMaxSpecCtas;  // sink-set CTAs per (sequence, KV head)
 
 // Share of the SMs the sink-set CTAs may take together (NUM / DEN).  More
@@ -87,11 +87,14 @@ constexpr size_t kAlign = 256;
 
 thread_local cudaError_t t_last_error = cudaSuccess;
 
-// Remember the most recent failing CUDA call of this thread.
+}  // namespace
+
 bool ok(cudaError_t e) {
     if (e != cudaSuccess) t_last_error = e;
     return e == cudaSuccess;
 }
+
+namespace {
 
 // Record an event so that, under stream capture, it becomes an event node
 // whose timestamp is taken at replay; outside capture it is a plain record.
@@ -149,6 +152,8 @@ alspec_status get_device_state(DeviceState** out) {
     return ALSPEC_OK;
 }
 
+}  // namespace
+
 int sm_count_for_plan() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) == cudaSuccess &&
@@ -156,6 +161,8 @@ int sm_count_for_plan() {
         return n;
     return 148;  // B200
 }
+
+namespace {
 
 // ------------------------------------------------------------- planning
 
@@ -432,18 +439,28 @@ void kernel_shape(int dtype, int D, int G, int engine, bool fused, int* threads,
 // cuTensorMapEncodeTiled from the driver, looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-alspec_status encode_kv_map(CUtensorMap* map, const void* base, const alspec_desc& d) {
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        if (!g_encode) {
-            cudaDriverEntryPointQueryResult q{};
-            void* fn = nullptr;
-            if (!ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q)) ||
-                q != cudaDriverEntryPointSuccess || !fn)
-                return ALSPEC_ERR_CUDA;
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-        }
+}  // namespace
+
+alspec_status tiled_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn_out) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_encode) {
+        cudaDriverEntryPointQueryResult q{};
+        void* fn = nullptr;
+        if (!ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q)) ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return ALSPEC_ERR_CUDA;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
+    *fn_out = g_encode;
+    return ALSPEC_OK;
+}
+
+namespace {
+
+alspec_status encode_kv_map(CUtensorMap* map, const void* base, const alspec_desc& d) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const alspec_status found = tiled_map_encoder(&encode);
+    if (found != ALSPEC_OK) return found;
     // A 2-D view of the cache: rows = (b, kv head, token), d columns; boxes of
     // 64 columns (128 bytes) x 32 rows with 128-byte swizzle.
     const cuuint64_t rows = (cuuint64_t)d.batch * d.n_kv_heads * d.max_seq_len;
@@ -451,10 +468,10 @@ alspec_status encode_kv_map(CUtensorMap* map, const void* base, const alspec_des
     const cuuint64_t strides[1] = {(cuuint64_t)d.head_dim * 2};
     const cuuint32_t box[2] = {64, 32};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ALSPEC_OK : ALSPEC_ERR_INVALID_ARG;
 }
 
@@ -502,12 +519,28 @@ alspec_status launch(KernelFn fn, dim3 grid, dim3 block, int smem, cudaStream_t 
     return ok(cudaLaunchKernelEx(&cfg, fn, p)) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Dynamic shared-memory attributes that smem_attr_once has set, by device.
+constexpr int kMaxAttr = 32;
+const void* g_attr[kMaxDevices][kMaxAttr] = {};
 
 // Forget the no-alloc scratch addresses looked up so far (alspec_shutdown).
 void noalloc_forget();
 
 }  // namespace
+
+alspec_status smem_attr_once(const void* kernel, int bytes) {
+    int dev = 0;
+    if (!ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return ALSPEC_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int i = 0;
+    while (i < kMaxAttr && g_attr[dev][i] && g_attr[dev][i] != kernel) ++i;
+    if (i < kMaxAttr && g_attr[dev][i] == kernel) return ALSPEC_OK;
+    if (!ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
+        return ALSPEC_ERR_CUDA;
+    if (i < kMaxAttr) g_attr[dev][i] = kernel;
+    return ALSPEC_OK;
+}
+
 }  // namespace alspec
 
 using namespace alspec;
@@ -988,6 +1021,7 @@ alspec_status alspec_graph_destroy(void* graph) {
 alspec_status alspec_shutdown(void) {
     noalloc_forget();
     std::lock_guard<std::mutex> lock(g_mutex);
+    std::memset(g_attr, 0, sizeof g_attr);
     int cur = 0;
     const bool have_cur = cudaGetDevice(&cur) == cudaSuccess;
     alspec_status st = ALSPEC_OK;

@@ -55,11 +55,11 @@
 
 #include <cstdint>
 
+#include "common.cuh"
 #include "ptx.cuh"
 
 namespace alspec {
 
-constexpr int kSmemLimit = 227 * 1024;
 // Sink-set CTAs per (sequence, KV head) at most: one portable cluster.
 constexpr int kMaxSpecCtas = 8;
 
@@ -84,19 +84,11 @@ constexpr int kMaxSpecCtas = 8;
 #define ALSPEC_MID_SPW 3
 #endif
 
-constexpr unsigned kErrSeqLen = 1u;   // ALSPEC_DEVERR_SEQ_LEN
-constexpr unsigned kErrTimeout = 2u;  // ALSPEC_DEVERR_TIMEOUT
-constexpr unsigned kErrBounds = 4u;   // ALSPEC_DEVERR_BOUNDS (debug build)
-
 // Counter words at the head of the workspace, then the per-sequence
 // tickets [B] (merge kernel: one per CTA of the sequence; one-launch
 // schedule: one per KV head), and for the one-launch schedule the per-head
 // tile tickets [B * Hkv].  Whoever takes the last ticket of a group resets
 // it, so the words are zero between calls.
-constexpr int kCtrQueue = 0;
-constexpr int kCtrDone = 1;
-constexpr int kCtrError = 2;
-constexpr int kCtrFixed = 4;
 
 __host__ __device__ __forceinline__ int ctr_seq(int B, int Hkv, int b) {
     (void)Hkv;
@@ -527,12 +519,6 @@ __global__ void __launch_bounds__(64) stalled_wait_kernel(const __grid_constant_
     }
 }
 
-// Weight of a partial with max m against the merged max M: exactly 1 when
-// m == M, so merging one partial with empty ones reproduces it bit for bit.
-__device__ __forceinline__ float merge_weight(float m, float M) {
-    return m == M ? 1.f : exp2f(m - M);
-}
-
 // ====================================================== CUDA-core engine
 
 template <class C, typename T>
@@ -720,11 +706,6 @@ struct CoreEngine {
 // written with 128-byte swizzle (rows of 128 bytes).
 __device__ __forceinline__ uint32_t swz(int r, int c) {
     return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <class C, int D, int G>

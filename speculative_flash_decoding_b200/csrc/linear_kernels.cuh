@@ -1,0 +1,280 @@
+// Linear layer of a decode batch on the fifth-generation tensor cores:
+// y = activation(x W^T + bias) + residual, bf16 operands, fp32 sums.
+//
+// The batch is small, so the operands change sides: 128 rows of W are the M
+// of a tcgen05.mma, up to 256 rows of x its N, and the accumulator is
+// y^T in TMEM (lane = feature, column = batch row).  W is read once from HBM
+// while x comes from L2; TMA brings 64-column slices of both (128-byte
+// swizzle) through a ring of up to 200 KB.  One warp's lane issues the
+// copies, one the MMAs, then four warps read the accumulator back for the
+// epilogue.  When there are fewer tiles than SMs, the CTAs of a cluster
+// split K and add their accumulators through distributed shared memory, each
+// for its share of the batch rows, in rank order (the same bits every time).
+// Bound by the bytes of W up to about 250 rows.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace alspec {
+
+constexpr int kLinThreads = 128;
+constexpr int kLinM = 128;        // features per tile
+constexpr int kLinK = 64;         // columns of a stage: 128 bytes
+constexpr int kLinMaxN = 256;     // batch rows per tile
+constexpr int kLinMaxStages = 12;
+constexpr int kLinRing = 200 * 1024;
+// More than half of an SM's shared memory whatever the sizes, so that an SM
+// holds one CTA and its TMEM allocation never waits for another's.
+constexpr int kLinMinSmem = 120 * 1024;
+
+struct LinearParams {
+    CUtensorMap tw, tx;  // 2-D: (k, row)
+    const __nv_bfloat16* bias;
+    const void* residual;
+    void* y;
+    int rows, n, kblocks;
+    int nt;        // batch rows per tile: a multiple of 16
+    int row_tiles, split, stages;
+    int tmem_cols;
+    int out_bf16, act;
+    unsigned* err;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ bool lin_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         const LinearParams& p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 31) == 0) {
+            if (*abort) return false;
+            if (global_ns() - t0 > p.timeout_ns) {
+                *abort = 1;
+                if (p.err) atomicOr(p.err, kErrTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+// Shared-memory matrix descriptor: K-major rows of 128 bytes with 128-byte
+// swizzle, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t lin_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+__device__ __forceinline__ void lin_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void lin_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+
+// 16 accumulator columns of this thread's lane.
+__device__ __forceinline__ void lin_load16(uint32_t addr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ float lin_activate(float x, int act) {
+    switch (act) {
+    case 1: return x < 0.f ? 0.f : x;
+    case 2: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+    case 3: return x / (1.f + expf(-x));
+    default: return x;
+    }
+}
+
+__device__ __forceinline__ float lin_residual(const LinearParams& p, long long i) {
+    return p.out_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[i])
+                      : static_cast<const float*>(p.residual)[i];
+}
+
+__device__ __forceinline__ void lin_store(const LinearParams& p, long long i, float v) {
+    if (p.out_bf16)
+        static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(p.y)[i] = v;
+}
+
+__global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
+    const __grid_constant__ LinearParams p) {
+    extern __shared__ unsigned char lin_raw[];
+    __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    volatile int* abort = &abort_flag;
+    unsigned char* ring = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(lin_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)blockIdx.x % p.split, tile = (int)blockIdx.x / p.split;
+    // Row tiles of one feature tile are neighbours: its W comes from L2 for
+    // all but the first.
+    const int n0 = tile / p.row_tiles * kLinM, r0 = tile % p.row_tiles * p.nt;
+    const int kb0 = (int)((long long)rank * p.kblocks / p.split);
+    const int kb1 = (int)((long long)(rank + 1) * p.kblocks / p.split);
+    const int stage_bytes = kLinM * 128 + p.nt * 128;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(&done, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tmap(&p.tw);
+        prefetch_tmap(&p.tx);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&tmem_base)),
+                     "r"((uint32_t)p.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+            int i = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++i) {
+                const int s = i % p.stages;
+                if (i >= p.stages && !lin_wait(empty + s, (i / p.stages - 1) & 1, abort, p)) break;
+                unsigned char* w = ring + s * stage_bytes;
+                mbar_arrive_expect_tx(full + s, (uint32_t)stage_bytes);
+                tma_load_2d(w, &p.tw, kb * kLinK, n0, full + s, p.row_tiles == 1 ? once : keep);
+                tma_load_2d(w + kLinM * 128, &p.tx, kb * kLinK, r0, full + s, keep);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // fp32 accumulator, bf16 operands, both K-major.
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                                   ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(kLinM >> 4) << 24);
+            for (int i = 0; i < kb1 - kb0; ++i) {
+                const int s = i % p.stages;
+                if (!lin_wait(full + s, (i / p.stages) & 1, abort, p)) {
+                    // Given up: let the copies in flight land (bounded).
+                    const uint64_t t0 = global_ns();
+                    for (int j = i; j < min(i + p.stages, kb1 - kb0); ++j)
+                        while (!mbar_try_wait(full + j % p.stages, (j / p.stages) & 1))
+                            if (global_ns() - t0 > p.timeout_ns) break;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t a = smem_addr(ring + s * stage_bytes);
+                const uint64_t da = lin_desc(a), db = lin_desc(a + kLinM * 128);
+#pragma unroll
+                for (int k = 0; k < kLinK / 16; ++k)  // 32 bytes of every row a step
+                    lin_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
+                lin_commit(empty + s);
+            }
+            lin_commit(&done);
+        }
+    }
+    __syncwarp();
+    // The accumulator is complete (each thread waits; bounded).
+    const bool good = lin_wait(&done, 0, abort, p) && !*abort;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    __syncthreads();
+
+    const int feature = n0 + (int)threadIdx.x;
+    const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+    if (p.split == 1) {
+        const bool live = feature < p.n && good;
+        const float bias = live && p.bias ? __bfloat162float(p.bias[feature]) : 0.f;
+        for (int c = 0; c < p.nt && r0 + c < p.rows; c += 16) {
+            float v[16], add[16];
+            lin_load16(taddr + c, v);
+            const int nr = live ? min(16, p.rows - r0 - c) : 0;
+            const long long at = (long long)(r0 + c) * p.n + feature;
+            if (p.residual) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < nr) add[i] = lin_residual(p, at + (long long)i * p.n);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (i < nr) {
+                    const float o = lin_activate(v[i] + bias, p.act);
+                    lin_store(p, at + (long long)i * p.n, p.residual ? o + add[i] : o);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        // This CTA's part of the sums, [batch row][feature], where the ring
+        // was; then every CTA of the cluster adds its share of the rows.
+        float* mine = reinterpret_cast<float*>(ring);
+        for (int c = 0; c < p.nt; c += 16) {
+            float v[16];
+            lin_load16(taddr + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + threadIdx.x] = v[i];
+        }
+        cluster_sync();
+        const int rows = min(p.nt, p.rows - r0);
+        const int c0 = (int)((long long)rank * rows / p.split);
+        const int c1 = (int)((long long)(rank + 1) * rows / p.split);
+        const bool live = feature < p.n && good;
+        const float bias = live && p.bias ? __bfloat162float(p.bias[feature]) : 0.f;
+        const uint32_t base = smem_addr(mine) + threadIdx.x * 4;
+        if (live) {
+            for (int c = c0; c < c1; ++c) {
+                float part[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < p.split) part[s] = ld_dsmem(dsmem_addr(base + c * kLinM * 4, s));
+                const long long at = (long long)(r0 + c) * p.n + feature;
+                const float add = p.residual ? lin_residual(p, at) : 0.f;
+                float sum = part[0];
+#pragma unroll
+                for (int s = 1; s < 8; ++s)
+                    if (s < p.split) sum += part[s];
+                const float o = lin_activate(sum + bias, p.act);
+                lin_store(p, at, p.residual ? o + add : o);
+            }
+        }
+        cluster_sync();
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"((uint32_t)p.tmem_cols)
+                     : "memory");
+}
+
+}  // namespace alspec

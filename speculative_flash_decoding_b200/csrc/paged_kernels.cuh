@@ -1,0 +1,1025 @@
+// Kernels of the paged key-value cache: writing rows (quantised for e4m3
+// pages), reading them back, and attention of one new token per sequence.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace alspec {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+
+// Element types of pages, sources and outputs (alspec_dtype).
+enum : int { kF32 = 0, kBf16 = 1, kE4m3 = 2 };
+
+// Where rows live in the pools.
+struct PageLayout {
+    long long page_stride, head_stride, token_stride;  // elements
+    int n_pages, page_size, hkv;
+
+    __device__ __forceinline__ long long row(int page, int head, int slot) const {
+        return page * page_stride + head * head_stride + slot * token_stride;
+    }
+    __device__ __forceinline__ long long scale(int page, int head, int slot) const {
+        return ((long long)page * hkv + head) * page_size + slot;
+    }
+};
+
+// Eight values as fp32, from fp32 or bf16 (16-byte aligned).
+template <int T>
+__device__ __forceinline__ void load8(const void* base, long long i, float (&x)[8]) {
+    if constexpr (T == kF32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+        const float4 a = __ldg(p), b = __ldg(p + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+        const uint4 r = __ldg(
+            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16);
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight values to fp32, or rounded to bf16 (16-byte aligned).
+template <int T>
+__device__ __forceinline__ void store8(void* base, long long i, const float (&x)[8]) {
+    if constexpr (T == kF32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + i) =
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                       pack_bf16(x[6], x[7]));
+    }
+}
+
+// ---------------------------------------------------------------- append
+
+struct AppendParams {
+    PageLayout lay;
+    void* pages[2];
+    float* scales[2];
+    const void* src[2];
+    long long src_stride[2];
+    const int* positions;
+    const int* seq_ids;
+    const int* table;
+    int n, batch, max_pages;
+    unsigned* err;
+};
+
+constexpr int kAppendThreads = 256;
+
+// D / 8 lanes hold one (token, KV head)'s row of K and of V, eight values
+// each, so every access is 8 to 32 bytes wide and amax is a few shuffles;
+// the source rows are loaded before the positions and the table have come
+// back.  Bound by latency for a decode step and by bytes for a prompt.
+template <int SRC, int DST, int D>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(
+    const __grid_constant__ AppendParams p) {
+    constexpr int LPR = D / 8;  // lanes per row
+    const long long idx = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
+    const long long pair = idx / LPR;  // (token, head)
+    const int col = (int)(idx % LPR) * 8;
+    const bool live = pair < (long long)p.n * p.lay.hkv;
+    const int t = live ? (int)(pair / p.lay.hkv) : 0;
+    const int h = live ? (int)(pair % p.lay.hkv) : 0;
+    float x[2][8];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+        load8<SRC>(p.src[w], t * p.src_stride[w] + (long long)h * D + col, x[w]);
+    const int pos = __ldg(p.positions + t);
+    const int seq = p.seq_ids ? __ldg(p.seq_ids + t) : t;
+    int page = -1;
+    if (live && pos >= 0) {
+        const int entry = pos / p.lay.page_size;
+        if (seq >= 0 && seq < p.batch && entry < p.max_pages)
+            page = __ldg(p.table + (long long)seq * p.max_pages + entry);
+        if (page < 0 || page >= p.lay.n_pages) {
+            page = -1;
+            if (p.err && col == 0) atomicOr(p.err, kErrPage);
+        }
+    }
+    const int slot = pos >= 0 ? pos % p.lay.page_size : 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        if constexpr (DST == kE4m3) {
+            // amax as an integer maximum of magnitudes: NaN is above
+            // infinity, so either one makes the scale, and with it the row,
+            // not finite.
+            uint32_t a = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[w][j]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            float s = __fdiv_rn(__uint_as_float(a), kE4m3Max);
+            s = s < kMinScale ? kMinScale : s;
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                c[j] = f32x2_to_e4m3x2(__fdiv_rn(x[w][2 * j], s), __fdiv_rn(x[w][2 * j + 1], s));
+            if (page >= 0) {
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.pages[w]) +
+                                          p.lay.row(page, h, slot) + col) =
+                    make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                if (col == 0) p.scales[w][p.lay.scale(page, h, slot)] = s;
+            }
+        } else if (page >= 0) {
+            store8<DST>(p.pages[w], p.lay.row(page, h, slot) + col, x[w]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gather
+
+struct GatherParams {
+    PageLayout lay;
+    const void* pages[2];
+    const float* scales[2];
+    const int* table;
+    const int* lens;
+    void* out[2];
+    int batch, max_pages, max_len, blocks_per_head;
+    unsigned* err;
+};
+
+constexpr int kGatherThreads = 256;
+constexpr int kGatherRows = 64;  // tokens per CTA
+
+// One CTA reads back 64 tokens of one (sequence, KV head), K and V; D / 8
+// lanes hold a row.  Bound by bytes.
+template <int SRC, int DST, int D>
+__global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
+    const __grid_constant__ GatherParams p) {
+    constexpr int LPR = D / 8;
+    constexpr int RPI = kGatherThreads / LPR;  // rows per iteration
+    const unsigned bh = blockIdx.x / p.blocks_per_head;
+    const int t0 = (int)(blockIdx.x % p.blocks_per_head) * kGatherRows;
+    const int b = bh / p.lay.hkv, h = bh % p.lay.hkv;
+    int len = __ldg(p.lens + b);
+    const long long cap = min((long long)p.max_len, (long long)p.max_pages * p.lay.page_size);
+    if (len < 0 || len > cap) {
+        if (p.err && threadIdx.x == 0 && t0 == 0 && h == 0) atomicOr(p.err, kErrSeqLen);
+        len = len < 0 ? 0 : (int)cap;
+    }
+    const int col = (int)(threadIdx.x % LPR) * 8;
+#pragma unroll
+    for (int i = 0; i < kGatherRows / RPI; ++i) {
+        const int t = t0 + i * RPI + (int)threadIdx.x / LPR;
+        if (t >= len) continue;
+        const int page = __ldg(p.table + (long long)b * p.max_pages + t / p.lay.page_size);
+        if (page < 0 || page >= p.lay.n_pages) {
+            if (p.err && col == 0) atomicOr(p.err, kErrPage);
+            continue;
+        }
+        const int slot = t % p.lay.page_size;
+        const long long src = p.lay.row(page, h, slot) + col;
+        const long long dst = ((long long)bh * p.max_len + t) * D + col;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float x[8];
+            if constexpr (SRC == kE4m3) {
+                const uint2 c = __ldg(reinterpret_cast<const uint2*>(
+                    static_cast<const uint8_t*>(p.pages[w]) + src));
+                const float s = __ldg(p.scales[w] + p.lay.scale(page, h, slot));
+                const uint32_t r[2] = {c.x, c.y};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t f = e4m3x2_to_f16x2((uint16_t)(r[j / 2] >> (16 * (j % 2))));
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                    x[2 * j] = v.x * s;
+                    x[2 * j + 1] = v.y * s;
+                }
+            } else {
+                load8<SRC>(p.pages[w], src, x);
+            }
+            store8<DST>(p.out[w], dst, x);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- decode
+//
+// Every warp of a persistent grid (one CTA per SM) owns an equal share of
+// the batch's tiles of 32 tokens, numbered (sequence, KV head, tile): the
+// share is found from seq_lens alone, so ragged batches are balanced to one
+// tile without a queue.  A warp streams its tiles through a ring of its own
+// (TMA boxes of up to 32 rows x 128 bytes, swizzled; it refills a stage as
+// soon as it has read it, so no other warp is waited for) and keeps the
+// running maximum, sum and weighted values of flash decoding.  A (sequence,
+// head) that ends inside one warp's share is written by that warp; one that
+// spans warps is joined in shared memory, one that spans CTAs by the last of
+// its CTAs to arrive (a ticket), in the order of the tiles, so the bits do
+// not depend on who joins.
+//
+// Products run on m16n8 MMAs with the (up to 8) query heads of a KV group as
+// rows 0-7 of A.  Rows 8-15 carry what the operand type rounds away, so that
+// P V (and Q K) keep more bits than one operand has:
+//   bf16 pages  Q is exact; P = hi + lo (16 bits), for fp32 outputs a third
+//               bf16 term in a second MMA (24 bits);
+//   e4m3 pages  codes widen exactly to f16; Q, scaled by a power of two per
+//               head, and P are f16 hi + lo (22 bits).  The K scale
+//               multiplies a score, the V scale a probability, which is kept
+//               in f16's range by a running power of two (vexp);
+//   fp32 pages  tf32 with hi + lo of both operands (22 bits).
+// Bound by HBM bytes; the ring of 192 KB keeps the SM's share of the memory
+// pipeline full while warps compute.
+
+constexpr int kTile = 32;       // tokens
+constexpr int kHeadRows = 8;    // query heads per work unit
+
+struct PagedParams {
+    CUtensorMap tk, tv;  // 4-D: (head_dim, slot, KV head, page)
+    const void* q;
+    long long q_stride;
+    const float* ks;
+    const float* vs;
+    const int* table;
+    const int* lens;
+    int batch, hq, hkv, group, blocks;  // blocks: work units of 8 heads per KV head
+    int max_pages, page_size, n_pages, box;
+    int cap;        // max_pages * page_size, at most 2^31 - 64
+    int S, W;
+    float qscale;   // scale * log2(e)
+    void* out;
+    int out_bf16;
+    float* lse;
+    unsigned* ctr;  // error word and the tickets of the joins
+    float* part;    // [CTA][2] partials
+    unsigned long long timeout_ns;
+};
+
+constexpr int kPagedTickets = kCtrFixed;  // one ticket per CTA follows
+
+template <int T, int D>
+struct PagedCfg {
+    static constexpr int ES = T == kF32 ? 4 : T == kBf16 ? 2 : 1;
+    static constexpr int RB = D * ES;                     // bytes of a row
+    static constexpr int SEGB = RB < 128 ? RB : 128;      // bytes of a box row
+    static constexpr int SEGS = RB / SEGB;                // boxes side by side
+    static constexpr int TILEB = kTile * RB;              // K or V of a tile
+    static constexpr int STAGEB = 2 * TILEB;
+    // Warps and stages per warp of a 192 KB ring (measured: see DESIGN).
+    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? 4 : STAGEB >= 8192 ? 6 : 8;
+    static constexpr int ST = 196608 / STAGEB / NW;
+    static constexpr int kThreads = NW * 32;
+    static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
+    static constexpr int kOffDeposit = NW * ST * STAGEB;
+    static constexpr int kOffScale = kOffDeposit + NW * PART * 4;
+    static constexpr int kOffMeta = kOffScale + (T == kE4m3 ? NW * ST * 2 * kTile * 4 : 0);
+    static constexpr int kOffBar = kOffMeta + NW * ST * 16;
+    static constexpr int kOffPiece = kOffBar + NW * ST * 8;
+    static constexpr int kOffMisc = kOffPiece + 2 * NW * 32;
+    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
+    static_assert(ST >= 2 && PART * 4 <= ST * STAGEB, "ring");
+    static_assert(kOffScale % 16 == 0 && kOffMeta % 16 == 0 && kOffBar % 8 == 0, "alignment");
+};
+
+// Tiles of one sequence: tile i covers tokens [32 i, 32 i + 32) for i < a and
+// [32 (i + f - a), ...) from there on; every tile holds a token of the set.
+struct PagedSeq {
+    int len, n, a, f;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int len) {
+    PagedSeq s;
+    s.len = min(max(len, 0), p.cap);
+    const int all = (s.len + kTile - 1) / kTile;
+    if (p.S + p.W == 0) {
+        s.a = s.n = all;
+        s.f = 0;
+    } else {
+        s.a = (min(p.S, s.len) + kTile - 1) / kTile;
+        const int w0 = max(0, s.len - p.W);
+        s.f = max(s.a, w0 / kTile);
+        s.n = s.a + (w0 < s.len ? all - s.f : 0);
+    }
+    return s;
+}
+
+// A tile's place: sequence, work unit (KV head and block of 8 query heads).
+struct PagedPos {
+    int b, u, i;
+    PagedSeq s;
+};
+
+// The place of tile x (0 <= x < total) in the numbering (sequence, unit,
+// tile); called by a whole warp.
+__device__ __forceinline__ PagedPos paged_find(const PagedParams& p, long long x) {
+    const int lane = threadIdx.x & 31;
+    const int units = p.hkv * p.blocks;
+    long long base = 0;
+    PagedPos r;
+    r.b = r.u = r.i = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b < p.batch ? paged_seq(p, __ldg(p.lens + b)).n : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, (base + incl) * units > x);
+        if (past) {
+            const int w = __ffs(past) - 1;
+            const int nw = __shfl_sync(0xffffffffu, n, w);
+            const long long before = base + __shfl_sync(0xffffffffu, incl, w) - nw;
+            const int off = (int)(x - before * units);
+            r.b = b0 + w;
+            r.u = off / nw;
+            r.i = off % nw;
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    r.s = paged_seq(p, __ldg(p.lens + r.b));
+    return r;
+}
+
+__device__ __forceinline__ long long paged_total(const PagedParams& p) {
+    long long n = 0;
+    for (int b = threadIdx.x & 31; b < p.batch; b += 32) n += paged_seq(p, __ldg(p.lens + b)).n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n * (p.hkv * p.blocks);
+}
+
+// Shares: the tiles are spread over `workers` warps, warp w owning
+// [w * total / workers, (w + 1) * total / workers).
+__device__ __forceinline__ long long share_begin(long long total, long long workers, long long w) {
+    return w * total / workers;
+}
+__device__ __forceinline__ long long share_of(long long total, long long workers, long long x) {
+    return ((x + 1) * workers - 1) / total;
+}
+
+// A run of tiles of one (sequence, unit) that did not end where it began.
+struct PagedPiece {
+    int b, u, lo, hi;  // tiles [lo, hi) of n; hi == 0: none
+    int n, pad[3];
+};
+
+// One finished element pair or quad of the output.
+__device__ __forceinline__ void paged_store(const PagedParams& p, long long i, float v) {
+    if (p.out_bf16)
+        static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(p.out)[i] = v;
+}
+
+// o / l, 0 where nothing was attended to.
+__device__ __forceinline__ float paged_ratio(float o, float l) { return l == 0.f ? 0.f : o / l; }
+
+__device__ __forceinline__ float paged_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int T, int D>
+struct PagedWarp {
+    using C = PagedCfg<T, D>;
+    static constexpr int KS = T == kF32 ? D / 8 : D / 16;  // k steps of Q K
+    static constexpr int NT = D / 8;                       // output n tiles
+    static constexpr bool kSplitQ = T != kBf16;
+
+    uint32_t qa[KS][2];                    // A rows 0-7
+    uint32_t qb[kSplitQ ? KS : 1][2];      // A rows 8-15: what qa's type rounds away
+    float acc[NT][4];                      // rows 0-7 and 8-15
+    float m, l;                            // this lane's head: maximum, share of the sum
+    float rowscale;                        // log2-domain factor of a score
+    float vexp;                            // e4m3: acc holds sums times 1 / vexp
+
+    __device__ __forceinline__ void reset() {
+        m = -INFINITY;
+        l = 0.f;
+        vexp = kMinScale;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    }
+
+    // Queries of unit u of sequence b; lanes of absent heads hold zeros.
+    __device__ __forceinline__ void load_q(const PagedParams& p, int b, int u, int lane) {
+        const int r = lane >> 2, j = lane & 3;
+        const int h0 = (u / p.blocks) * p.group, blk = (u % p.blocks) * kHeadRows;
+        const bool live = blk + r < p.group;
+        const long long at = b * p.q_stride + (long long)(h0 + (live ? blk + r : 0)) * D;
+        rowscale = p.qscale;
+        if constexpr (T == kBf16) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(
+                static_cast<const __nv_bfloat16*>(p.q) + at);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qa[k][0] = live ? __ldg(q + 8 * k + j) : 0u;
+                qa[k][1] = live ? __ldg(q + 8 * k + j + 4) : 0u;
+            }
+        } else if constexpr (T == kE4m3) {
+            // Lane j of a quad holds elements 16 k + 4 j .. + 3 of k step k:
+            // the order in which the codes of K come out of ldmatrix.
+            const uint2* q = reinterpret_cast<const uint2*>(
+                static_cast<const __nv_bfloat16*>(p.q) + at);
+            uint2 raw[KS];
+            uint32_t a = 0;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                raw[k] = live ? __ldg(q + 4 * k + j) : make_uint2(0u, 0u);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t x = w ? raw[k].y : raw[k].x;
+                    a = max(a, max((x << 16) & 0x7fff0000u, x & 0x7fff0000u));
+                }
+            }
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            // 2^e >= the row's largest magnitude, e in [-125, 127].
+            const int e = min(max((int)(a >> 23) - 126, -125), 127);
+            const float inv = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23) *
+                              (e == 127 ? 0.5f : 1.f);
+            rowscale = p.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t x = w ? raw[k].y : raw[k].x;
+                    split_f16(__uint_as_float(x << 16) * inv,
+                              __uint_as_float(x & 0xffff0000u) * inv, qa[k][w], qb[k][w]);
+                }
+        } else {
+            const float* q = static_cast<const float*>(p.q) + at;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+                    split_tf32(live ? __ldg(q + 8 * k + j + 4 * w) : 0.f, qa[k][w], qb[k][w]);
+        }
+    }
+
+    __device__ __forceinline__ static void split_f16(float x, float y, uint32_t& hi, uint32_t& lo) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        lo = pack_f16(x - f.x, y - f.y);
+    }
+    __device__ __forceinline__ static void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo,
+                                                      float& rx, float& ry) {
+        hi = pack_bf16(x, y);
+        const float dx = x - __uint_as_float(hi << 16), dy = y - __uint_as_float(hi & 0xffff0000u);
+        lo = pack_bf16(dx, dy);
+        rx = dx - __uint_as_float(lo << 16);
+        ry = dy - __uint_as_float(lo & 0xffff0000u);
+    }
+    __device__ __forceinline__ static void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+        hi = __float_as_uint(x) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+    }
+
+    // Shared-memory address of 16-byte chunk c of row r of a swizzled tile.
+    __device__ __forceinline__ static uint32_t chunk(uint32_t tile, int r, int c) {
+        if constexpr (C::SEGB == 128)
+            return tile + (uint32_t)((c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        else
+            return tile + (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    }
+
+    // One tile: `mask` bit t says whether token t counts (the rows of V of
+    // the others are zero), ks and vs are the tile's scales.
+    __device__ __forceinline__ void tile(const PagedParams& p, uint32_t k_smem, uint32_t v_smem,
+                                         unsigned mask, const float* ks, const float* vs,
+                                         int lane) {
+        const int row8 = lane & 7, mat = lane >> 3, j = lane & 3;
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+            const int r = 8 * n + row8;
+#pragma unroll
+            for (int c = 0; c < C::RB / 16; c += 4) {
+                uint32_t f[4];
+                ldsm_x4(chunk(k_smem, r, c + mat), f[0], f[1], f[2], f[3]);
+                if constexpr (T == kBf16) {
+                    mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[0], f[1]);
+                    mma_bf16_16816(s[n], qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, f[2], f[3]);
+                } else if constexpr (T == kE4m3) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_f16_16816(s[n], qa[c + i][0], qb[c + i][0], qa[c + i][1], qb[c + i][1],
+                                      e4m3x2_to_f16x2((uint16_t)f[i]),
+                                      e4m3x2_to_f16x2((uint16_t)(f[i] >> 16)));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = c / 2 + i;
+                        uint32_t h0, l0, h1, l1;
+                        split_tf32(__uint_as_float(f[2 * i]), h0, l0);
+                        split_tf32(__uint_as_float(f[2 * i + 1]), h1, l1);
+                        mma_tf32_1688(s[n], qa[k][0], qb[k][0], qa[k][1], qb[k][1], h0, h1);
+                        mma_tf32_1688(s[n], qa[k][0], qb[k][0], qa[k][1], qb[k][1], l0, l1);
+                    }
+                }
+            }
+        }
+        // Scores in the log2 domain; lane (r, j) holds head r, tokens
+        // 8 n + 2 j and + 1.
+        float x[4][2], vsc[4][2], mx = -INFINITY, vmax = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 8 * n + 2 * j + i;
+                const bool on = (mask >> t) & 1u;
+                float y = (kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i]) * rowscale;
+                if constexpr (T == kE4m3) {
+                    y *= ks[t];
+                    vsc[n][i] = on ? vs[t] : 0.f;
+                    vmax = fmaxf(vmax, fabsf(vsc[n][i]));
+                }
+                x[n][i] = on ? y : -INFINITY;
+                mx = fmaxf(mx, x[n][i]);
+            }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m, mx);
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = exp2f(m - base);  // 1 where the maximum stands
+        float rescale = alpha, vinv = 1.f;
+        if constexpr (T == kE4m3) {
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+            // The power of two at or below the largest V scale so far.
+            const float v2 = fmaxf(
+                vexp, __uint_as_float(min(__float_as_uint(vmax), 0x7f000000u) & 0x7f800000u));
+            rescale = alpha * (vexp / v2);
+            vexp = v2;
+            vinv = 1.f / v2;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[n][i] = exp2f(x[n][i] - base);
+                sum += x[n][i];
+                if constexpr (T == kE4m3) x[n][i] *= vsc[n][i] * vinv;
+            }
+        m = m_new;
+        l = l * alpha + sum;
+        if (__any_sync(0xffffffffu, rescale != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[i][k] *= rescale;
+        }
+        // O += P V.
+        if constexpr (T == kF32) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {  // tokens 8 n ..: k step n
+                uint32_t h0, l0, h1, l1;
+                split_tf32(x[n][0], h0, l0);
+                split_tf32(x[n][1], h1, l1);
+                const int r0 = 8 * n + 2 * j;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int d = 8 * i + (lane >> 2);
+                    uint32_t a0, a1, b0, b1;
+                    split_tf32(lds(chunk(v_smem, r0, d >> 2) + (d & 3) * 4), a0, a1);
+                    split_tf32(lds(chunk(v_smem, r0 + 1, d >> 2) + (d & 3) * 4), b0, b1);
+                    mma_tf32_1688(acc[i], h0, l0, h1, l1, a0, b0);
+                    mma_tf32_1688(acc[i], h0, l0, h1, l1, a1, b1);
+                }
+            }
+        } else {
+            const bool third = T == kBf16 && !p.out_bf16;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // tokens 16 k ..
+                uint32_t a[4], c0 = 0, c1 = 0;
+                if constexpr (T == kE4m3) {
+                    split_f16(x[2 * k][0], x[2 * k][1], a[0], a[1]);
+                    split_f16(x[2 * k + 1][0], x[2 * k + 1][1], a[2], a[3]);
+                } else {
+                    float r0, r1, r2, r3;
+                    split_bf16(x[2 * k][0], x[2 * k][1], a[0], a[1], r0, r1);
+                    split_bf16(x[2 * k + 1][0], x[2 * k + 1][1], a[2], a[3], r2, r3);
+                    c0 = pack_bf16(r0, r1);
+                    c1 = pack_bf16(r2, r3);
+                }
+                // Matrices of one ldmatrix: tokens 0-7 and 8-15 of the step,
+                // chunks c and c + 1.
+                const int r = 16 * k + (mat & 1) * 8 + row8;
+#pragma unroll
+                for (int c = 0; c < C::RB / 16; c += 2) {
+                    uint32_t f[4];
+                    ldsm_x4_t(chunk(v_smem, r, c + (mat >> 1)), f[0], f[1], f[2], f[3]);
+                    if constexpr (T == kE4m3) {
+                        // A code pair of one token per half word: split into
+                        // the even and the odd column's tokens.
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const uint32_t g0 = __byte_perm(f[2 * w], 0u, 0x3120);
+                            const uint32_t g1 = __byte_perm(f[2 * w + 1], 0u, 0x3120);
+                            mma_f16_16816(acc[2 * (c + w)], a[0], a[1], a[2], a[3],
+                                          e4m3x2_to_f16x2((uint16_t)g0),
+                                          e4m3x2_to_f16x2((uint16_t)g1));
+                            mma_f16_16816(acc[2 * (c + w) + 1], a[0], a[1], a[2], a[3],
+                                          e4m3x2_to_f16x2((uint16_t)(g0 >> 16)),
+                                          e4m3x2_to_f16x2((uint16_t)(g1 >> 16)));
+                        }
+                    } else {
+                        mma_bf16_16816(acc[c], a[0], a[1], a[2], a[3], f[0], f[1]);
+                        mma_bf16_16816(acc[c + 1], a[0], a[1], a[2], a[3], f[2], f[3]);
+                        if (third) {
+                            mma_bf16_16816(acc[c], c0, 0u, c1, 0u, f[0], f[1]);
+                            mma_bf16_16816(acc[c + 1], c0, 0u, c1, 0u, f[2], f[3]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ static float lds(uint32_t addr) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+        return v;
+    }
+
+    // Calls f(column, value) for this lane's elements of its head's row.
+    template <typename F>
+    __device__ __forceinline__ void each(int lane, F f) const {
+        const int j = lane & 3;
+#pragma unroll
+        for (int i = 0; i < NT; i += 2)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float v = acc[i + w][k] + acc[i + w][k + 2];
+                    if constexpr (T == kE4m3) v *= vexp;
+                    const int col = T == kE4m3 ? 8 * i + 4 * j + 2 * k + w : 8 * (i + w) + 2 * j + k;
+                    f(col, v);
+                }
+    }
+
+    // The row sum of the exponentials over the quad's lanes.
+    __device__ __forceinline__ float row_sum() const {
+        float s = l + __shfl_xor_sync(0xffffffffu, l, 1);
+        return s + __shfl_xor_sync(0xffffffffu, s, 2);
+    }
+
+    // Partial of this warp: m[8], l[8], o[8][D].
+    __device__ __forceinline__ void deposit(float* dst, int lane) const {
+        const float s = row_sum();
+        const int r = lane >> 2;
+        if ((lane & 3) == 0) {
+            dst[r] = m;
+            dst[kHeadRows + r] = s;
+        }
+        float* o = dst + 2 * kHeadRows + r * D;
+        each(lane, [&](int col, float v) { o[col] = v; });
+    }
+
+    __device__ __forceinline__ void write_out(const PagedParams& p, int b, int u, int lane) const {
+        const float s = row_sum();
+        const int head = (u / p.blocks) * p.group + (u % p.blocks) * kHeadRows + (lane >> 2);
+        if ((u % p.blocks) * kHeadRows + (lane >> 2) >= p.group) return;
+        const long long at = (long long)b * p.hq + head;
+        if (p.lse && (lane & 3) == 0) p.lse[at] = paged_lse(m, s);
+        each(lane, [&](int col, float v) { paged_store(p, at * D + col, paged_ratio(v, s)); });
+    }
+};
+
+template <int T, int D>
+__global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kernel(
+    const __grid_constant__ PagedParams p) {
+    using C = PagedCfg<T, D>;
+    extern __shared__ unsigned char pd_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(pd_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::kOffPiece);
+    volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
+
+    // Padded rows of the batch, and lengths out of range.
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        const int len = __ldg(p.lens + b);
+        if ((len < 0 || len > p.cap) && threadIdx.x == 0) atomicOr(p.ctr + kCtrError, kErrSeqLen);
+        if (len > 0) continue;
+        for (int i = threadIdx.x; i < p.hq * D; i += C::kThreads)
+            paged_store(p, (long long)b * p.hq * D + i, 0.f);
+        for (int i = threadIdx.x; p.lse && i < p.hq; i += C::kThreads)
+            p.lse[(long long)b * p.hq + i] = -INFINITY;
+    }
+
+    const long long total = paged_total(p);
+    if (total == 0) return;
+    const long long workers = min((long long)gridDim.x * C::NW, total);
+    if ((long long)blockIdx.x * C::NW >= workers) return;
+    const long long w = (long long)blockIdx.x * C::NW + warp;
+    const long long x0 = w < workers ? share_begin(total, workers, w) : 0;
+    const int tiles = w < workers ? (int)(share_begin(total, workers, w + 1) - x0) : 0;
+
+    if (lane == 0) {
+        for (int s = 0; s < C::ST; ++s) mbar_init(bars + warp * C::ST + s, T == kE4m3 ? 33 : 1);
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 0) misc[0] = 0;
+    __syncthreads();
+
+    unsigned char* ring = smem + warp * C::ST * C::STAGEB;
+    uint64_t* full = bars + warp * C::ST;
+    int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * C::ST;
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * kTile;
+    float* deposit0 = reinterpret_cast<float*>(smem + C::kOffDeposit) + warp * C::PART;
+    const int units = p.hkv * p.blocks;
+
+    if (tiles > 0) {
+        PagedPos pos = paged_find(p, x0);
+        {
+            const PagedPos end = paged_find(p, x0 + tiles - 1);
+            if (lane == 0) {
+                PagedPiece head{}, tail{};
+                tail.b = end.b, tail.u = end.u, tail.n = end.s.n;
+                if (end.b == pos.b && end.u == pos.u) {
+                    if (pos.i > 0 || end.i + 1 < end.s.n) tail.lo = pos.i, tail.hi = end.i + 1;
+                } else {
+                    if (pos.i > 0)
+                        head.b = pos.b, head.u = pos.u, head.lo = pos.i, head.hi = head.n = pos.s.n;
+                    if (end.i + 1 < end.s.n) tail.lo = 0, tail.hi = end.i + 1;
+                }
+                pieces[2 * warp] = head;
+                pieces[2 * warp + 1] = tail;
+            }
+        }
+        const uint64_t pol = l2_evict_first_policy();
+        // A box is `box` rows of one 128-byte column segment of K or V; the
+        // boxes of a tile are spread over the lanes: lane = sub-box +
+        // boxes-down * (segment, K or V).
+        const int down = kTile / p.box;
+        const int sub = lane & (down - 1), first = lane / down, step = kTile / down;
+        int page = 0;  // of this lane's sub-box in the next tile to be issued
+        auto token0 = [&](const PagedPos& q) {
+            return (q.i < q.s.a ? q.i : q.i + q.s.f - q.s.a) * kTile;
+        };
+        auto fetch_page = [&]() {
+            const int t = token0(pos) + sub * p.box;
+            if (t < pos.s.len)
+                page = __ldg(p.table + (long long)pos.b * p.max_pages + t / p.page_size);
+        };
+        auto issue = [&](int slot) {
+            const int t0 = token0(pos);
+            const int boxes = min(down, (pos.s.len - t0 + p.box - 1) / p.box);
+            int pg = page;
+            if (sub < boxes && (pg < 0 || pg >= p.n_pages)) {
+                atomicOr(p.ctr + kCtrError, kErrPage);
+                pg = 0;
+            }
+            const int t = t0 + sub * p.box;
+            const int in_page = t % p.page_size;
+            const int h = pos.u / p.blocks;
+            unsigned char* stage = ring + slot * C::STAGEB;
+            if (lane == 0) {
+                meta[slot] = make_int4(pos.b, pos.u, pos.i, t0);
+                mbar_arrive_expect_tx(full + slot, (uint32_t)(boxes * p.box * 2 * C::RB));
+            }
+            __syncwarp();
+            if (sub < boxes) {
+                for (int c = first; c < 2 * C::SEGS; c += step) {
+                    const int v = c & 1, seg = c >> 1;
+                    tma_load_4d(stage + v * C::TILEB + seg * kTile * C::SEGB +
+                                    sub * p.box * C::SEGB,
+                                v ? &p.tv : &p.tk, seg * (C::SEGB / C::ES), in_page, h, pg,
+                                full + slot, pol);
+                }
+            }
+            if constexpr (T == kE4m3) {
+                // Lane = token: its scales, and its arrival once they landed.
+                const int mine = lane / p.box;
+                const int pg_t = __shfl_sync(0xffffffffu, pg, mine);
+                const int in_t = __shfl_sync(0xffffffffu, in_page, mine) + lane % p.box;
+                if (t0 + lane < pos.s.len) {
+                    const long long at = ((long long)pg_t * p.hkv + h) * p.page_size + in_t;
+                    cp_async_4(scales + slot * 2 * kTile + lane, p.ks + at);
+                    cp_async_4(scales + slot * 2 * kTile + kTile + lane, p.vs + at);
+                }
+                cp_async_arrive(full + slot);
+            }
+            // On to the next tile; its page numbers are on their way while
+            // this one streams.
+            if (++pos.i == pos.s.n) {
+                pos.i = 0;
+                if (++pos.u == units) {
+                    pos.u = 0;
+                    do {
+                        ++pos.b;
+                        pos.s = paged_seq(p, pos.b < p.batch ? __ldg(p.lens + pos.b) : 0);
+                    } while (pos.b < p.batch && pos.s.n == 0);
+                }
+            }
+            fetch_page();
+        };
+        fetch_page();
+        int issued = 0;
+        for (; issued < min(C::ST, tiles); ++issued) issue(issued);
+
+        PagedWarp<T, D> state;
+        PagedSeq s{};
+        int done = 0;
+        bool lost = false, have0 = false, have1 = false;
+        for (; done < tiles; ++done) {
+            const int slot = done % C::ST;
+            // Bounded wait for the fill.
+            uint64_t since = 0;
+            for (uint32_t it = 0; !lost; ++it) {
+                if (__all_sync(0xffffffffu, mbar_try_wait(full + slot, (done / C::ST) & 1))) break;
+                if ((it & 31) == 31) {
+                    const uint64_t now = __shfl_sync(0xffffffffu, global_ns(), 0);
+                    if (since == 0) since = now;
+                    lost = now - since > p.timeout_ns;
+                }
+            }
+            if (lost) break;
+            const int4 at = meta[slot];
+            if (done == 0 || at.z == 0) {
+                s = paged_seq(p, __ldg(p.lens + at.x));
+                state.reset();
+                state.load_q(p, at.x, at.y, lane);
+            }
+            // Tokens of the set: bit t of the mask.
+            const int t = at.w + lane;
+            const bool on = t < s.len &&
+                            (p.S + p.W == 0 || t < p.S || t >= s.len - p.W);
+            const unsigned mask = __ballot_sync(0xffffffffu, on);
+            const uint32_t k_smem = smem_addr(ring + slot * C::STAGEB);
+            const uint32_t v_smem = k_smem + C::TILEB;
+            if (mask != 0xffffffffu) {
+                // Rows of V that do not count may hold anything: zeros, so
+                // that 0 * NaN does not reach the sums.
+                if (!on) {
+                    unsigned char* v = ring + slot * C::STAGEB + C::TILEB + lane * C::SEGB;
+                    for (int g = 0; g < C::SEGS; ++g)
+                        for (int c = 0; c < C::SEGB / 16; ++c)
+                            *reinterpret_cast<uint4*>(v + g * kTile * C::SEGB + c * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const float* sc = scales + slot * 2 * kTile;
+            state.tile(p, k_smem, v_smem, mask, sc, sc + kTile, lane);
+            __syncwarp();
+            const bool last = done + 1 == tiles;
+            if (issued < tiles) {
+                issue(slot);
+                ++issued;
+            }
+            if (last || at.z + 1 == s.n) {
+                const bool whole = done >= at.z && at.z + 1 == s.n;
+                if (whole) {
+                    state.write_out(p, at.x, at.y, lane);
+                } else if (last) {
+                    state.deposit(reinterpret_cast<float*>(ring), lane);
+                    have1 = true;
+                } else {
+                    state.deposit(deposit0, lane);
+                    have0 = true;
+                }
+            }
+        }
+        if (lost) {
+            // Nothing more is asked for; let what was asked for land (bounded).
+            if (lane == 0) atomicOr(p.ctr + kCtrError, kErrTimeout);
+            for (int n = done; n < issued; ++n) {
+                const uint64_t t0 = global_ns();
+                while (!mbar_try_wait(full + n % C::ST, (n / C::ST) & 1))
+                    if (global_ns() - t0 > p.timeout_ns) break;
+            }
+            __syncwarp();
+            // Empty partials, so that the joins stay complete.
+            state.reset();
+            if (!have0) state.deposit(deposit0, lane);
+            if (!have1) state.deposit(reinterpret_cast<float*>(ring), lane);
+        }
+    } else if (lane == 0) {
+        pieces[2 * warp] = PagedPiece{};
+        pieces[2 * warp + 1] = PagedPiece{};
+    }
+    __syncthreads();
+
+    // Join what spans warps: runs of pieces of one (sequence, unit).
+    auto partial = [&](int i) {
+        return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * C::ST * C::STAGEB)
+                       : reinterpret_cast<const float*>(smem + C::kOffDeposit) + (i >> 1) * C::PART;
+    };
+    for (int i = 0; i < 2 * C::NW;) {
+        const PagedPiece a = pieces[i];
+        if (a.hi == 0) {
+            ++i;
+            continue;
+        }
+        int k = i, hi = 0;
+        for (; k < 2 * C::NW; ++k) {
+            if (pieces[k].hi == 0) continue;
+            if (pieces[k].b != a.b || pieces[k].u != a.u) break;
+            hi = pieces[k].hi;
+        }
+        const bool whole = a.lo == 0 && hi == a.n;
+        const int rows = min(kHeadRows, p.group - (a.u % p.blocks) * kHeadRows);
+        const long long head0 = (long long)a.b * p.hq + (a.u / p.blocks) * p.group +
+                                (a.u % p.blocks) * kHeadRows;
+        // A run that began in an earlier CTA is this CTA's first partial, one
+        // that goes on in the next its second.
+        float* mine = p.part + ((long long)blockIdx.x * 2 + (a.lo == 0 ? 1 : 0)) * C::PART;
+        for (int e = threadIdx.x; e < rows * D; e += C::kThreads) {
+            const int r = e / D;
+            float M = -INFINITY;
+            for (int n = i; n < k; ++n)
+                if (pieces[n].hi) M = fmaxf(M, partial(n)[r]);
+            float o = 0.f, l = 0.f;
+            for (int n = i; n < k; ++n) {
+                if (!pieces[n].hi) continue;
+                const float* q = partial(n);
+                const float f = merge_weight(q[r], M);
+                o += q[2 * kHeadRows + e] * f;
+                l += q[kHeadRows + r] * f;
+            }
+            if (whole) {
+                paged_store(p, head0 * D + e, paged_ratio(o, l));
+                if (p.lse && e % D == 0) p.lse[head0 + r] = paged_lse(M, l);
+            } else {
+                __stcg(mine + 2 * kHeadRows + e, o);
+                if (e % D == 0) {
+                    __stcg(mine + r, M);
+                    __stcg(mine + kHeadRows + r, l);
+                }
+            }
+        }
+        if (!whole) {
+            // The last CTA of this (sequence, unit) to arrive joins it.
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                // Tile 0 of the run in the numbering, from one of its tiles.
+                const int at = i >> 1;
+                const long long begin =
+                    share_begin(total, workers, (long long)blockIdx.x * C::NW + at) +
+                    ((i & 1) && pieces[i].lo == 0
+                         ? share_begin(total, workers, (long long)blockIdx.x * C::NW + at + 1) -
+                               share_begin(total, workers, (long long)blockIdx.x * C::NW + at) -
+                               pieces[i].hi
+                         : 0) -
+                    pieces[i].lo;
+                const int c0 = (int)(share_of(total, workers, begin) / C::NW);
+                const int c1 = (int)(share_of(total, workers, begin + a.n - 1) / C::NW);
+                __threadfence();
+                const unsigned old = atom_add_acq_rel_gpu(p.ctr + kPagedTickets + c0, 1u);
+                misc[1] = old == (unsigned)(c1 - c0) ? 1 : 0;
+                misc[2] = c0;
+                misc[3] = c1;
+                if (old == (unsigned)(c1 - c0)) p.ctr[kPagedTickets + c0] = 0u;
+                __threadfence();
+            }
+            __syncthreads();
+            if (misc[1]) {
+                const int c0 = misc[2], c1 = misc[3];
+                for (int e = threadIdx.x; e < rows * D; e += C::kThreads) {
+                    const int r = e / D;
+                    float M = -INFINITY, o = 0.f, l = 0.f;
+                    for (int c = c0; c <= c1; ++c)
+                        M = fmaxf(M, __ldcg(p.part + ((long long)c * 2 + (c == c0)) * C::PART + r));
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* q = p.part + ((long long)c * 2 + (c == c0)) * C::PART;
+                        const float f = merge_weight(__ldcg(q + r), M);
+                        o += __ldcg(q + 2 * kHeadRows + e) * f;
+                        l += __ldcg(q + kHeadRows + r) * f;
+                    }
+                    paged_store(p, head0 * D + e, paged_ratio(o, l));
+                    if (p.lse && e % D == 0) p.lse[head0 + r] = paged_lse(M, l);
+                }
+            }
+            __syncthreads();
+        }
+        i = k;
+    }
+}
+
+}  // namespace alspec

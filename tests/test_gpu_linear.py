@@ -1,0 +1,145 @@
+"""The linear layer with its epilogue on the GPU against its 64-bit form."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+U = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+
+
+def _inputs(rows, n, k, pad=0, seed=0, bias=True, residual=None):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, k + pad), generator=g).to(BF16).cuda()[:, :k]
+    w = (torch.randn((n, k), generator=g) / math.sqrt(k)).to(BF16).cuda()
+    b = torch.randn(n, generator=g).to(BF16).cuda() if bias else None
+    r = torch.randn((rows, n), generator=g).to(residual).cuda() if residual else None
+    return x, w, b, r
+
+
+ACT = {"none": lambda y: y, "relu": lambda y: y.clamp(min=0),
+       "gelu": lambda y: 0.5 * y * (1 + torch.erf(y / math.sqrt(2))),
+       "silu": lambda y: y * torch.sigmoid(y)}
+# The largest slope of each activation, and what its own evaluation loses
+# relative to its argument (erff and expf: a few units of 2^-23).
+SLOPE = {"none": 1.0, "relu": 1.0, "gelu": 1.13, "silu": 1.1}
+
+
+def _check(y, x, w, b, r, act):
+    x, w = x.double(), w.double()
+    z = x @ w.t()
+    size = x.abs() @ w.abs().t()
+    if b is not None:
+        z, size = z + b.double(), size + b.double().abs()
+    want = ACT[act](z)
+    if r is not None:
+        want = want + r.double()
+    # fp32 sums of k exact products in steps of 16, each step losing at most
+    # 2^-23 of the running magnitude, and up to 8 more for the split, bias and
+    # residual; 2^-21 for the activation; the output's rounding.
+    k = x.shape[1]
+    extra = 0 if r is None else r.double().abs() * 2.0 ** -23
+    bound = (SLOPE[act] * size * (k / 16 + 16) * 2.0 ** -23 + size * 2.0 ** -21 + extra
+             + U[y.dtype] * want.abs() + 1e-37)
+    err = (y.double() - want).abs()
+    assert bool((err <= bound).all()), f"largest error / bound {(err / bound).max():.3g}"
+
+
+@pytest.mark.parametrize("rows,n,k,act,out,bias,residual,pad", [
+    (1, 1, 8, "none", F32, True, True, 0),
+    (1, 4096, 4096, "none", F32, False, True, 0),
+    (1, 130, 72, "relu", BF16, True, False, 8),
+    (3, 257, 520, "gelu", F32, True, True, 0),
+    (16, 128, 64, "none", F32, False, False, 0),
+    (17, 1000, 4104, "silu", BF16, True, True, 64),
+    (33, 6144, 4096, "none", BF16, True, False, 0),
+    (64, 2048, 1024, "gelu", BF16, False, False, 0),
+    (250, 512, 8192, "silu", F32, True, True, 0),
+    (256, 384, 200, "relu", BF16, True, True, 0),
+    (257, 300, 96, "none", F32, True, False, 0),
+    (700, 129, 1032, "silu", BF16, True, True, 8),
+    (2, 20000, 136, "none", F32, True, False, 0),
+])
+def test_linear(cuda_device, rows, n, k, act, out, bias, residual, pad):
+    from speculative_flash_decoding_b200 import Linear
+    x, w, b, r = _inputs(rows, n, k, pad, seed=rows + n, bias=bias,
+                         residual=out if residual else None)
+    layer = Linear(w, bias=b, activation=act)
+    y = torch.full((rows, n), 9.0, dtype=out, device="cuda")
+    assert layer.apply(x, residual=r, out=y) is y
+    assert layer.device_error() == (0, 0)
+    _check(y, x, w, b, r, act)
+    again = layer.apply(x, residual=r, out=torch.empty_like(y))
+    assert torch.equal(again, y)
+
+
+def test_residual_in_place_and_guards(cuda_device):
+    from speculative_flash_decoding_b200 import Linear
+    rows, n, k = 5, 203, 328
+    x, w, b, _ = _inputs(rows, n, k)
+    buf = torch.randn(rows * n + 512, device="cuda")
+    keep = buf.clone()
+    y = buf[256: 256 + rows * n].view(rows, n)
+    r = y.clone()
+    Linear(w, bias=b).apply(x, residual=y, out=y)
+    _check(y, x, w, b, r, "none")
+    assert torch.equal(buf[:256], keep[:256]) and torch.equal(buf[-256:], keep[-256:])
+
+
+def test_rows_of_one_do_not_touch_others(cuda_device):
+    """NaN in one row of x stays in that row of y, in one row of W in that
+    column."""
+    from speculative_flash_decoding_b200 import Linear
+    x, w, _, _ = _inputs(20, 150, 96, bias=False)
+    x[7, 3] = math.nan
+    w[149, 0] = math.nan
+    y = Linear(w).apply(x, out_dtype=F32)
+    bad = torch.zeros(20, 150, dtype=torch.bool, device="cuda")
+    bad[7] = True
+    bad[:, 149] = True
+    assert torch.equal(y.isnan(), bad)
+    z = Linear(w, activation="relu").apply(x, out_dtype=F32)
+    assert torch.equal(z.isnan(), bad)
+
+
+def test_activation_far_out(cuda_device):
+    """Large arguments of either sign, and infinities."""
+    from speculative_flash_decoding_b200 import Linear
+    w = torch.eye(8, device="cuda").to(BF16)
+    x = torch.tensor([[0.0, 1e30, -1e30, 100.0, -100.0, -88.0, 1e-30, -1e-30]], device="cuda").to(BF16)
+    for act in ("gelu", "silu", "relu"):
+        y = Linear(w, activation=act).apply(x, out_dtype=F32)
+        want = ACT[act](x.double())
+        assert bool(((y.double() - want).abs() <= 2.0 ** -20 * x.double().abs()).all()), act
+
+
+def test_no_rows(cuda_device):
+    from speculative_flash_decoding_b200 import Linear
+    _, w, b, _ = _inputs(1, 64, 64)
+    assert Linear(w, bias=b).apply(torch.empty(0, 64, dtype=BF16, device="cuda")).shape == (0, 64)
+
+
+def test_captured_and_on_two_streams(cuda_device):
+    from speculative_flash_decoding_b200 import Linear
+    x, w, b, r = _inputs(9, 600, 512, residual=BF16)
+    layer = Linear(w, bias=b, activation="silu")
+    y = torch.zeros(9, 600, dtype=BF16, device="cuda")
+    layer.apply(x, residual=r, out=y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.apply(x, residual=r, out=y)
+    x.copy_(torch.randn(9, 512, generator=torch.Generator().manual_seed(9)).to(BF16))
+    g.replay()
+    torch.cuda.synchronize()
+    _check(y, x, w, b, r, "silu")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ys = [torch.zeros_like(y) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, o in zip(streams, ys):
+            layer.apply(x, residual=r, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o in ys:
+        assert torch.equal(o, y)

@@ -1,0 +1,182 @@
+"""What the paged-cache and linear entry points refuse on the host, before
+anything is launched (no GPU needed), and the quantisation rule."""
+import ctypes
+import math
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import speculative_flash_decoding_b200 as sfd
+from speculative_flash_decoding_b200 import alspec as ab
+from paged_reference import quantise
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, WORKSPACE = (ab.ALSPEC_OK, ab.ALSPEC_ERR_INVALID_ARG,
+                                       ab.ALSPEC_ERR_UNSUPPORTED, ab.ALSPEC_ERR_WORKSPACE)
+P = 1 << 20  # stands for a device address
+
+
+def cache(**kw):
+    f = dict(k_pages=P, v_pages=P, k_scales=P, v_scales=P, page_stride=0, head_stride=0,
+             token_stride=0, n_pages=10, page_size=16, n_kv_heads=4, head_dim=128,
+             dtype=ab.ALSPEC_BF16, reserved=0)
+    f.update(kw)
+    return ab.alspec_paged_cache(**f)
+
+
+def append(c, **kw):
+    a = dict(k=P, v=P, src=ab.ALSPEC_BF16, ks=0, vs=0, pos=P, seq=P, n=4, table=P, batch=3,
+             pages=5, err=P)
+    a.update(kw)
+    return ab.alspec_paged_append(c, a["k"], a["v"], a["src"], a["ks"], a["vs"], a["pos"],
+                                  a["seq"], a["n"], a["table"], a["batch"], a["pages"], a["err"],
+                                  0)
+
+
+def gather(c, **kw):
+    a = dict(table=P, pages=5, lens=P, batch=3, length=70, dtype=ab.ALSPEC_BF16, k=P, v=P, err=P)
+    a.update(kw)
+    return ab.alspec_paged_gather(c, a["table"], a["pages"], a["lens"], a["batch"], a["length"],
+                                  a["dtype"], a["k"], a["v"], a["err"], 0)
+
+
+def decode(c, **kw):
+    a = dict(q=P, qs=0, hq=8, table=P, pages=5, lens=P, batch=3, S=0, W=0, scale=0.0,
+             dtype=ab.ALSPEC_F32, out=P, lse=P, ms=0, ws=P, wsb=1 << 30)
+    a.update(kw)
+    return ab.alspec_paged_decode(c, a["q"], a["qs"], a["hq"], a["table"], a["pages"], a["lens"],
+                                  a["batch"], a["S"], a["W"], a["scale"], a["dtype"], a["out"],
+                                  a["lse"], a["ms"], a["ws"], a["wsb"], 0)
+
+
+def linear(**kw):
+    a = dict(x=P, xs=0, w=P, bias=P, res=P, y=P, dtype=ab.ALSPEC_BF16, act=0, rows=4, n=100,
+             k=64, err=P)
+    a.update(kw)
+    return ab.alspec_linear(a["x"], a["xs"], a["w"], a["bias"], a["res"], a["y"], a["dtype"],
+                            a["act"], a["rows"], a["n"], a["k"], a["err"], 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k_pages=0), INVALID), (dict(v_pages=0), INVALID), (dict(k_pages=P + 8), INVALID),
+    (dict(n_pages=0), INVALID), (dict(page_size=0), INVALID), (dict(n_kv_heads=0), INVALID),
+    (dict(head_dim=-1), INVALID), (dict(dtype=3), INVALID), (dict(reserved=1), INVALID),
+    (dict(head_dim=96), UNSUPPORTED), (dict(page_size=12), UNSUPPORTED),
+    (dict(page_size=1), UNSUPPORTED),
+    (dict(dtype=ab.ALSPEC_E4M3, k_scales=0), INVALID),
+    (dict(dtype=ab.ALSPEC_E4M3, v_scales=P + 2), INVALID),
+    # Strides: one missing, rows that overlap, not a multiple of 16 bytes.
+    (dict(page_stride=8192), INVALID),
+    (dict(page_stride=8192, head_stride=2048, token_stride=64), INVALID),
+    (dict(page_stride=8192, head_stride=2048, token_stride=132), INVALID),
+    (dict(page_stride=8192, head_stride=2052, token_stride=128), INVALID),
+    (dict(page_stride=1 << 40, head_stride=2048, token_stride=128), INVALID),
+    (dict(page_stride=-8192, head_stride=2048, token_stride=128), INVALID),
+])
+def test_every_entry_point_refuses_a_bad_cache(kw, code):
+    c = cache(**kw)
+    assert append(c) == code and gather(c) == code and decode(c) == code
+    if not any(s in kw for s in ("k_pages", "v_pages", "k_scales", "v_scales")):
+        assert ab.alspec_paged_workspace_size(c, 3, 8) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=0), INVALID), (dict(v=P + 4), INVALID), (dict(src=ab.ALSPEC_E4M3), INVALID),
+    (dict(ks=511), INVALID), (dict(vs=516), INVALID), (dict(vs=256), INVALID),
+    (dict(pos=0), INVALID), (dict(pos=P + 2), INVALID), (dict(seq=P + 1), INVALID),
+    (dict(seq=0, n=4), INVALID),          # more tokens than sequences
+    (dict(n=-1), INVALID), (dict(table=0), INVALID), (dict(table=P + 2), INVALID),
+    (dict(batch=0), INVALID), (dict(pages=0), INVALID), (dict(err=P + 3), INVALID),
+    (dict(n=0, k=0, v=0), OK),
+])
+def test_append_refuses(kw, code):
+    assert append(cache(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(table=0), INVALID), (dict(lens=0), INVALID), (dict(lens=P + 2), INVALID),
+    (dict(batch=0), INVALID), (dict(length=0), INVALID), (dict(dtype=ab.ALSPEC_E4M3), INVALID),
+    (dict(k=0), INVALID), (dict(v=P + 4), INVALID), (dict(err=P + 1), INVALID),
+    (dict(batch=1 << 20, length=1 << 20), UNSUPPORTED),
+])
+def test_gather_refuses(kw, code):
+    assert gather(cache(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=0), INVALID), (dict(q=P + 8), INVALID), (dict(qs=1000), INVALID),
+    (dict(qs=1028), INVALID), (dict(hq=6), INVALID), (dict(hq=0), INVALID),
+    (dict(table=0), INVALID), (dict(pages=0), INVALID), (dict(lens=0), INVALID),
+    (dict(batch=0), INVALID), (dict(batch=65536), UNSUPPORTED), (dict(S=-1), INVALID),
+    (dict(W=-1), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
+    (dict(dtype=ab.ALSPEC_E4M3), INVALID), (dict(out=0), INVALID), (dict(out=P + 4), INVALID),
+    (dict(lse=P + 2), INVALID), (dict(ms=-1), INVALID), (dict(ws=0), WORKSPACE),
+    (dict(ws=P + 4), WORKSPACE), (dict(wsb=4096), WORKSPACE),
+])
+def test_decode_refuses(kw, code):
+    assert decode(cache(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=0), INVALID), (dict(x=P + 8), INVALID), (dict(w=0), INVALID), (dict(w=P + 2), INVALID),
+    (dict(y=0), INVALID), (dict(y=P + 1), INVALID), (dict(bias=P + 1), INVALID),
+    (dict(res=P + 1), INVALID), (dict(dtype=ab.ALSPEC_F32, y=P + 2), INVALID),
+    (dict(dtype=ab.ALSPEC_E4M3), INVALID), (dict(act=4), INVALID), (dict(act=-1), INVALID),
+    (dict(rows=-1), INVALID), (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(k=68), INVALID),
+    (dict(xs=32), INVALID), (dict(xs=68), INVALID), (dict(err=P + 2), INVALID),
+    (dict(rows=0, x=0, y=0), OK),
+])
+def test_linear_refuses(kw, code):
+    assert linear(**kw) == code
+
+
+def test_workspace_does_not_grow_with_the_batch():
+    c = cache()
+    n = ab.alspec_paged_workspace_size(c, 1, 8)
+    assert n > 0 and n % 256 == 0
+    assert ab.alspec_paged_workspace_size(c, 4096, 32) == n
+    assert ab.alspec_paged_workspace_size(c, 1, 6) == 0
+
+
+def test_python_layer_refuses_without_a_gpu():
+    x = torch.zeros(4, 2, 16, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        sfd.PagedCache.from_tensors(x, x)
+    with pytest.raises(ValueError, match="dtype"):
+        sfd.PagedCache(4, 16, 2, 64, "int8")
+    with pytest.raises(ValueError, match="weight"):
+        sfd.Linear(torch.zeros(8, 8, dtype=torch.bfloat16))
+
+
+def test_quantisation_rule_on_the_cpu():
+    """scale = max(amax / 448, 2^-126); the largest value becomes 448, zeros
+    stay zero, and the value read back is within half an e4m3 step (2^-4
+    relative, 2^-10 of the scale for the smallest codes)."""
+    x = torch.randn(50, 3, 64, generator=torch.Generator().manual_seed(0))
+    x[0, 0] = 0
+    code, s = quantise(x)
+    assert code.float()[0, 0].abs().max() == 0 and s[0, 0] == 2.0 ** -126
+    top = code.float().abs().amax(-1)
+    assert bool((top[1:] == 448).all())
+    back = code.double() * s.double()[..., None]
+    bound = torch.maximum(x.abs().double() * 2.0 ** -4, s.double()[..., None] * 2.0 ** -10)
+    assert bool(((back - x.double()).abs() <= bound * (1 + 2.0 ** -20)).all())
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="gcc not installed")
+def test_c_sees_the_same_cache_description(tmp_path):
+    src = tmp_path / "size.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "alspec.h"\nint main(void) '
+                   '{ printf("%zu %zu %zu\\n", sizeof(alspec_paged_cache), '
+                   'offsetof(alspec_paged_cache, page_stride), '
+                   'offsetof(alspec_paged_cache, dtype)); return 0; }\n')
+    exe = tmp_path / "size"
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    assert got == [ctypes.sizeof(ab.alspec_paged_cache), ab.alspec_paged_cache.page_stride.offset,
+                   ab.alspec_paged_cache.dtype.offset]
