@@ -27,6 +27,16 @@ alspec_status tiled_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 // (set once per device, until alspec_shutdown).
 alspec_status smem_attr_once(const void* kernel, int bytes);
 
+// Launch attribute of a kernel that may be placed while the one ahead on the
+// stream still runs; it waits (griddepcontrol.wait) before it touches
+// anything that one reads or writes.
+inline cudaLaunchAttribute programmatic_launch() {
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace alspec

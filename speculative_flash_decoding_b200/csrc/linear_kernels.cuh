@@ -6,7 +6,7 @@
 // y^T in TMEM (lane = feature, column = batch row).  W is read once from HBM
 // while x comes from L2; TMA brings 64-column slices of both (128-byte
 // swizzle) through a ring of up to 200 KB.  One warp's lane issues the
-// copies, one the MMAs, then four warps read the accumulator back for the
+// copies, one the MMAs, then eight warps read the accumulator back for the
 // epilogue.  When there are fewer tiles than SMs, the CTAs of a cluster
 // split K and add their accumulators through distributed shared memory, each
 // for its share of the batch rows, in rank order (the same bits every time).
@@ -23,7 +23,7 @@
 
 namespace alspec {
 
-constexpr int kLinThreads = 128;
+constexpr int kLinThreads = 256;
 constexpr int kLinM = 128;        // features per tile
 constexpr int kLinK = 64;         // columns of a stage: 128 bytes
 constexpr int kLinMaxN = 256;     // batch rows per tile
@@ -103,25 +103,57 @@ __device__ __forceinline__ void lin_load16(uint32_t addr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ float lin_activate(float x, int act) {
-    switch (act) {
-    case 1: return x < 0.f ? 0.f : x;
-    case 2: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-    case 3: return x / (1.f + expf(-x));
-    default: return x;
+// The activation of N sums: one branch on its kind, not one per sum.
+template <int N>
+__device__ __forceinline__ void lin_activate(float (&x)[N], int act) {
+    if (act == 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = x[i] < 0.f ? 0.f : x[i];
+    } else if (act == 2) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = 0.5f * x[i] * (1.f + erff(x[i] * 0.70710678118654752f));
+    } else if (act == 3) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = x[i] / (1.f + expf(-x[i]));
     }
 }
 
-__device__ __forceinline__ float lin_residual(const LinearParams& p, long long i) {
-    return p.out_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[i])
-                      : static_cast<const float*>(p.residual)[i];
+__device__ __forceinline__ float lin_value(const float* p) { return *p; }
+__device__ __forceinline__ float lin_value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void lin_put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void lin_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Bias, activation and residual of the sums of one feature in `count` <= N
+// batch rows from r on, and their way out.
+template <typename O, int N>
+__device__ __forceinline__ void lin_finish(const LinearParams& p, float (&v)[N], int r, int count,
+                                           int feature, float bias) {
+    const long long at = (long long)r * p.n + feature;
+    const O* res = p.residual ? static_cast<const O*>(p.residual) + at : nullptr;
+    O* y = static_cast<O*>(p.y) + at;
+    float add[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        add[i] = res && i < count ? lin_value(res + (long long)i * p.n) : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += bias;
+    lin_activate(v, p.act);
+    if (res) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += add[i];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < count) lin_put(y + (long long)i * p.n, v[i]);
 }
 
-__device__ __forceinline__ void lin_store(const LinearParams& p, long long i, float v) {
+template <int N>
+__device__ __forceinline__ void lin_out(const LinearParams& p, float (&v)[N], int r, int count,
+                                        int feature, float bias) {
     if (p.out_bf16)
-        static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v);
+        lin_finish<__nv_bfloat16>(p, v, r, count, feature, bias);
     else
-        static_cast<float*>(p.y)[i] = v;
+        lin_finish<float>(p, v, r, count, feature, bias);
 }
 
 __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
@@ -164,6 +196,11 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_base;
+    // Launched while the kernel ahead on the stream may still run: nothing is
+    // read or written before it has completed, and only then may the next
+    // one be launched.
+    pdl_wait_prerequisite();
+    pdl_launch_dependents();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -210,61 +247,48 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     __syncthreads();
 
-    const int feature = n0 + (int)threadIdx.x;
-    const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+    // Warp w reads the 32 lanes of its quarter; the two halves of the warps
+    // take alternate groups of 16 columns.
+    const int quarter = warp & 3, half = warp >> 2;
+    const int fl = quarter * 32 + lane;  // feature within the tile
+    const int feature = n0 + fl;
+    const bool live = feature < p.n && good;
+    const float bias = live && p.bias ? __bfloat162float(p.bias[feature]) : 0.f;
+    const int rows = min(p.nt, p.rows - r0);
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
     if (p.split == 1) {
-        const bool live = feature < p.n && good;
-        const float bias = live && p.bias ? __bfloat162float(p.bias[feature]) : 0.f;
-        for (int c = 0; c < p.nt && r0 + c < p.rows; c += 16) {
-            float v[16], add[16];
+        for (int c = 16 * half; c < rows; c += 32) {
+            float v[16];
             lin_load16(taddr + c, v);
-            const int nr = live ? min(16, p.rows - r0 - c) : 0;
-            const long long at = (long long)(r0 + c) * p.n + feature;
-            if (p.residual) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < nr) add[i] = lin_residual(p, at + (long long)i * p.n);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (i < nr) {
-                    const float o = lin_activate(v[i] + bias, p.act);
-                    lin_store(p, at + (long long)i * p.n, p.residual ? o + add[i] : o);
-                }
-            }
+            if (live) lin_out(p, v, r0 + c, min(16, rows - c), feature, bias);
             __syncwarp();
         }
     } else {
         // This CTA's part of the sums, [batch row][feature], where the ring
         // was; then every CTA of the cluster adds its share of the rows.
         float* mine = reinterpret_cast<float*>(ring);
-        for (int c = 0; c < p.nt; c += 16) {
+        for (int c = 16 * half; c < rows; c += 32) {
             float v[16];
             lin_load16(taddr + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + threadIdx.x] = v[i];
+            for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + fl] = v[i];
         }
         cluster_sync();
-        const int rows = min(p.nt, p.rows - r0);
-        const int c0 = (int)((long long)rank * rows / p.split);
-        const int c1 = (int)((long long)(rank + 1) * rows / p.split);
-        const bool live = feature < p.n && good;
-        const float bias = live && p.bias ? __bfloat162float(p.bias[feature]) : 0.f;
-        const uint32_t base = smem_addr(mine) + threadIdx.x * 4;
+        const int c1 = (rank + 1) * rows / p.split;
+        const uint32_t base = smem_addr(mine) + fl * 4;
         if (live) {
-            for (int c = c0; c < c1; ++c) {
-                float part[8];
+            for (int c = rank * rows / p.split + 8 * half; c < c1; c += 16) {
+                float v[8];
+                for (int s = 0; s < p.split; ++s) {
+                    const uint32_t at = dsmem_addr(base + c * kLinM * 4, s);
+                    float part[8];
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    if (s < p.split) part[s] = ld_dsmem(dsmem_addr(base + c * kLinM * 4, s));
-                const long long at = (long long)(r0 + c) * p.n + feature;
-                const float add = p.residual ? lin_residual(p, at) : 0.f;
-                float sum = part[0];
+                    for (int i = 0; i < 8; ++i)
+                        part[i] = c + i < c1 ? ld_dsmem(at + i * kLinM * 4) : 0.f;
 #pragma unroll
-                for (int s = 1; s < 8; ++s)
-                    if (s < p.split) sum += part[s];
-                const float o = lin_activate(sum + bias, p.act);
-                lin_store(p, at, p.residual ? o + add : o);
+                    for (int i = 0; i < 8; ++i) v[i] = s == 0 ? part[i] : v[i] + part[i];
+                }
+                lin_out(p, v, r0 + c, min(8, c1 - c), feature, bias);
             }
         }
         cluster_sync();

@@ -127,17 +127,26 @@ PagedKernel paged_kernel() {
 }
 
 template <int D>
-PagedKernel paged_kernel_for(int dtype) {
-    return dtype == ALSPEC_F32    ? paged_kernel<kF32, D>()
-           : dtype == ALSPEC_BF16 ? paged_kernel<kBf16, D>()
-                                  : paged_kernel<kE4m3, D>();
+PagedKernel paged_kernel_for(int dtype, int out_dtype) {
+    return dtype == ALSPEC_F32        ? paged_kernel<kPagesF32, D>()
+           : dtype == ALSPEC_E4M3     ? paged_kernel<kPagesE4m3, D>()
+           : out_dtype == ALSPEC_BF16 ? paged_kernel<kPagesBf16, D>()
+                                      : paged_kernel<kPagesBf16Wide, D>();
 }
 
-// Workspace: the error word and one ticket per CTA, then two partials per CTA.
-size_t ticket_bytes(int ctas) { return ((size_t)(kPagedTickets + ctas) * 4 + 255) / 256 * 256; }
+// Workspace: the error word and one ticket per CTA, two partials per CTA for
+// other CTAs and one per warp for its own.
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t ticket_bytes(int ctas) { return align256((size_t)(kPagedTickets + ctas) * 4); }
+
+size_t part_bytes(const PagedKernel& k, int ctas) {
+    return align256((size_t)ctas * 2 * k.part_floats * 4);
+}
 
 size_t workspace_bytes_for(const PagedKernel& k, int ctas) {
-    return ticket_bytes(ctas) + ((size_t)ctas * 2 * k.part_floats * 4 + 255) / 256 * 256;
+    return ticket_bytes(ctas) + part_bytes(k, ctas) +
+           align256((size_t)ctas * (k.threads / 32) * k.part_floats * 4);
 }
 
 alspec_status check_heads(const alspec_paged_cache* c, int batch, int n_q_heads) {
@@ -266,8 +275,8 @@ alspec_status alspec_paged_gather(const alspec_paged_cache* cache, const int32_t
 
 size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, int n_q_heads) {
     if (check_heads(cache, batch, n_q_heads) != ALSPEC_OK) return 0;
-    const PagedKernel k = cache->head_dim == 128 ? paged_kernel_for<128>(cache->dtype)
-                                                 : paged_kernel_for<64>(cache->dtype);
+    const PagedKernel k = cache->head_dim == 128 ? paged_kernel_for<128>(cache->dtype, ALSPEC_F32)
+                                                 : paged_kernel_for<64>(cache->dtype, ALSPEC_F32);
     return workspace_bytes_for(k, sm_count_for_plan());
 }
 
@@ -291,8 +300,9 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
                           q_stride >= ((int64_t)1 << 40)))
         return ALSPEC_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return ALSPEC_ERR_WORKSPACE;
-    const PagedKernel kern = cache->head_dim == 128 ? paged_kernel_for<128>(cache->dtype)
-                                                    : paged_kernel_for<64>(cache->dtype);
+    const PagedKernel kern = cache->head_dim == 128
+                                 ? paged_kernel_for<128>(cache->dtype, out_dtype)
+                                 : paged_kernel_for<64>(cache->dtype, out_dtype);
     const int ctas = sm_count_for_plan();
     if (workspace_bytes < workspace_bytes_for(kern, ctas)) return ALSPEC_ERR_WORKSPACE;
     if ((st = smem_attr_once(reinterpret_cast<const void*>(kern.fn), kern.smem)) != ALSPEC_OK)
@@ -322,16 +332,36 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
     // No sequence is longer than cap, so neither term says more.
     p.S = std::min(n_sink, p.cap);
     p.W = std::min(window, p.cap);
-    p.qscale = (float)(1.4426950408889634 *
-                       (scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)cache->head_dim)));
+    // t / page_size for t < 2^31: with 2^(k - 1) < page_size <= 2^k, mul =
+    // ceil(2^(31 + k) / page_size) makes (t * mul) >> (31 + k) exact.
+    unsigned k = 0;
+    while ((1ull << k) < (unsigned long long)cache->page_size) ++k;
+    p.page_mul = (unsigned)(((1ull << (31 + k)) + cache->page_size - 1) / cache->page_size);
+    p.page_shift = k - 1;
+    // A factor above zero keeps masked scores (-inf) what they are; the sign
+    // goes to the queries.
+    const double factor = 1.4426950408889634 *
+                          (scale != 0.f ? std::fabs((double)scale)
+                                        : 1.0 / std::sqrt((double)cache->head_dim));
+    p.qscale = std::max((float)factor, kMinScale);
+    p.qflip = scale < 0.f ? 0x80000000u : 0u;
     p.out = out;
     p.out_bf16 = out_dtype == ALSPEC_BF16;
     p.lse = lse;
     p.ctr = static_cast<unsigned*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(ctas));
+    p.heads = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(ctas) +
+                                       part_bytes(kern, ctas));
     p.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
-    kern.fn<<<ctas, kern.threads, kern.smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return ok(cudaGetLastError()) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)kern.threads);
+    cfg.dynamicSmemBytes = kern.smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr = programmatic_launch();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return ok(cudaLaunchKernelEx(&cfg, kern.fn, p)) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 // soon as it has read it, so no other warp is waited for) and keeps the
 // running maximum, sum and weighted values of flash decoding.  A (sequence,
 // head) that ends inside one warp's share is written by that warp; one that
-// spans warps is joined in shared memory, one that spans CTAs by the last of
-// its CTAs to arrive (a ticket), in the order of the tiles, so the bits do
-// not depend on who joins.
+// spans warps is joined by its CTA, one that spans CTAs by the last of its
+// CTAs to arrive (a ticket), in the order of the tiles, so the bits do not
+// depend on who joins.
 //
 // Products run on m16n8 MMAs with the (up to 8) query heads of a KV group as
 // rows 0-7 of A.  Rows 8-15 carry what the operand type rounds away, so that
@@ -240,11 +240,16 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 //               multiplies a score, the V scale a probability, which is kept
 //               in f16's range by a running power of two (vexp);
 //   fp32 pages  tf32 with hi + lo of both operands (22 bits).
-// Bound by HBM bytes; the ring of 192 KB keeps the SM's share of the memory
-// pipeline full while warps compute.
+// Bound by HBM bytes while a scheduler has two or more warps: with one warp
+// each (4 warps a CTA) a warp's own latency bounded it (an instruction every
+// 5 cycles; 128K tokens of bf16 112 us instead of the figure below).
 
 constexpr int kTile = 32;       // tokens
 constexpr int kHeadRows = 8;    // query heads per work unit
+
+// Page types of the decode kernel: bf16 pages with fp32 outputs carry a
+// third term of P.
+enum : int { kPagesF32 = 0, kPagesBf16 = 1, kPagesE4m3 = 2, kPagesBf16Wide = 3 };
 
 struct PagedParams {
     CUtensorMap tk, tv;  // 4-D: (head_dim, slot, KV head, page)
@@ -256,14 +261,17 @@ struct PagedParams {
     const int* lens;
     int batch, hq, hkv, group, blocks;  // blocks: work units of 8 heads per KV head
     int max_pages, page_size, n_pages, box;
-    int cap;        // max_pages * page_size, at most 2^31 - 64
+    unsigned page_mul, page_shift;      // t / page_size = umulhi(t, page_mul) >> page_shift
+    int cap;        // max_pages * page_size, below 2^31
     int S, W;
-    float qscale;   // scale * log2(e)
+    float qscale;   // |scale| * log2(e)
+    unsigned qflip; // sign bit where scale is negative
     void* out;
     int out_bf16;
     float* lse;
     unsigned* ctr;  // error word and the tickets of the joins
-    float* part;    // [CTA][2] partials
+    float* part;    // [CTA][2] partials for other CTAs
+    float* heads;   // [CTA][warp] partials of a warp's first run
     unsigned long long timeout_ns;
 };
 
@@ -271,27 +279,27 @@ constexpr int kPagedTickets = kCtrFixed;  // one ticket per CTA follows
 
 template <int T, int D>
 struct PagedCfg {
-    static constexpr int ES = T == kF32 ? 4 : T == kBf16 ? 2 : 1;
+    static constexpr int ES = T == kPagesF32 ? 4 : T == kPagesE4m3 ? 1 : 2;
     static constexpr int RB = D * ES;                     // bytes of a row
     static constexpr int SEGB = RB < 128 ? RB : 128;      // bytes of a box row
     static constexpr int SEGS = RB / SEGB;                // boxes side by side
+    static constexpr int SEG_TILE = kTile * SEGB;         // one segment of a tile
     static constexpr int TILEB = kTile * RB;              // K or V of a tile
     static constexpr int STAGEB = 2 * TILEB;
-    // Warps and stages per warp of a 192 KB ring (measured: see DESIGN).
-    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? 4 : STAGEB >= 8192 ? 6 : 8;
+    // Warps, and stages per warp, of a 192 KB ring.
+    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? 6 : STAGEB >= 8192 ? 8 : 16;
     static constexpr int ST = 196608 / STAGEB / NW;
     static constexpr int kThreads = NW * 32;
     static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
-    static constexpr int kOffDeposit = NW * ST * STAGEB;
-    static constexpr int kOffScale = kOffDeposit + NW * PART * 4;
-    static constexpr int kOffMeta = kOffScale + (T == kE4m3 ? NW * ST * 2 * kTile * 4 : 0);
+    static constexpr int kOffScale = NW * ST * STAGEB;
+    static constexpr int kOffMeta = kOffScale + (T == kPagesE4m3 ? NW * ST * 2 * kTile * 4 : 0);
     static constexpr int kOffBar = kOffMeta + NW * ST * 16;
     static constexpr int kOffPiece = kOffBar + NW * ST * 8;
     static constexpr int kOffMisc = kOffPiece + 2 * NW * 32;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
     static_assert(ST >= 2 && PART * 4 <= ST * STAGEB, "ring");
-    static_assert(kOffScale % 16 == 0 && kOffMeta % 16 == 0 && kOffBar % 8 == 0, "alignment");
+    static_assert(kOffMeta % 16 == 0 && kOffPiece % 16 == 0, "alignment");
 };
 
 // Tiles of one sequence: tile i covers tokens [32 i, 32 i + 32) for i < a and
@@ -344,10 +352,10 @@ __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, long long x
             const int w = __ffs(past) - 1;
             const int nw = __shfl_sync(0xffffffffu, n, w);
             const long long before = base + __shfl_sync(0xffffffffu, incl, w) - nw;
-            const int off = (int)(x - before * units);
+            const unsigned off = (unsigned)(x - before * units);
             r.b = b0 + w;
-            r.u = off / nw;
-            r.i = off % nw;
+            r.u = off / (unsigned)nw;
+            r.i = off % (unsigned)nw;
             break;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -358,6 +366,7 @@ __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, long long x
 
 __device__ __forceinline__ long long paged_total(const PagedParams& p) {
     long long n = 0;
+#pragma unroll 4
     for (int b = threadIdx.x & 31; b < p.batch; b += 32) n += paged_seq(p, __ldg(p.lens + b)).n;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -379,27 +388,36 @@ struct PagedPiece {
     int n, pad[3];
 };
 
-// One finished element pair or quad of the output.
-__device__ __forceinline__ void paged_store(const PagedParams& p, long long i, float v) {
+// Two neighbouring elements of the output.
+__device__ __forceinline__ void paged_store2(const PagedParams& p, long long i, float x, float y) {
     if (p.out_bf16)
-        static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + i) = pack_bf16(x, y);
     else
-        static_cast<float*>(p.out)[i] = v;
+        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + i) = make_float2(x, y);
 }
 
-// o / l, 0 where nothing was attended to.
-__device__ __forceinline__ float paged_ratio(float o, float l) { return l == 0.f ? 0.f : o / l; }
+// 1 / l, 0 where nothing was attended to.
+__device__ __forceinline__ float paged_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 __device__ __forceinline__ float paged_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// 2^x to 2 ulp (0 below the normal range).
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int T, int D>
 struct PagedWarp {
     using C = PagedCfg<T, D>;
-    static constexpr int KS = T == kF32 ? D / 8 : D / 16;  // k steps of Q K
-    static constexpr int NT = D / 8;                       // output n tiles
-    static constexpr bool kSplitQ = T != kBf16;
+    static constexpr bool kB16 = T == kPagesBf16 || T == kPagesBf16Wide;
+    static constexpr int KS = T == kPagesF32 ? D / 8 : D / 16;  // k steps of Q K
+    static constexpr int NT = D / 8;                            // output n tiles
+    static constexpr int CH = C::RB / 16;                       // 16-byte chunks of a row
+    static constexpr bool kSplitQ = !kB16;
 
     uint32_t qa[KS][2];                    // A rows 0-7
     uint32_t qb[kSplitQ ? KS : 1][2];      // A rows 8-15: what qa's type rounds away
@@ -407,6 +425,17 @@ struct PagedWarp {
     float m, l;                            // this lane's head: maximum, share of the sum
     float rowscale;                        // log2-domain factor of a score
     float vexp;                            // e4m3: acc holds sums times 1 / vexp
+    uint32_t k_off, v_off;                 // this lane's part of a fragment's address
+
+    __device__ __forceinline__ void init(int lane) {
+        const int row8 = lane & 7, mat = lane >> 3, j = lane & 3;
+        const int sw = C::SEGB == 128 ? row8 : (row8 >> 1) & 3;
+        k_off = (uint32_t)(row8 * C::SEGB + ((mat ^ sw) << 4));
+        if constexpr (T == kPagesF32)
+            v_off = (uint32_t)(2 * j * 128 + (((lane >> 4) ^ (2 * j)) << 4) + ((lane >> 2) & 3) * 4);
+        else
+            v_off = (uint32_t)((mat & 1) * 8 * C::SEGB + row8 * C::SEGB + (((mat >> 1) ^ sw) << 4));
+    }
 
     __device__ __forceinline__ void reset() {
         m = -INFINITY;
@@ -425,15 +454,16 @@ struct PagedWarp {
         const bool live = blk + r < p.group;
         const long long at = b * p.q_stride + (long long)(h0 + (live ? blk + r : 0)) * D;
         rowscale = p.qscale;
-        if constexpr (T == kBf16) {
+        if constexpr (kB16) {
             const uint32_t* q = reinterpret_cast<const uint32_t*>(
                 static_cast<const __nv_bfloat16*>(p.q) + at);
+            const uint32_t flip = p.qflip | p.qflip >> 16;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                qa[k][0] = live ? __ldg(q + 8 * k + j) : 0u;
-                qa[k][1] = live ? __ldg(q + 8 * k + j + 4) : 0u;
+                qa[k][0] = live ? __ldg(q + 8 * k + j) ^ flip : 0u;
+                qa[k][1] = live ? __ldg(q + 8 * k + j + 4) ^ flip : 0u;
             }
-        } else if constexpr (T == kE4m3) {
+        } else if constexpr (T == kPagesE4m3) {
             // Lane j of a quad holds elements 16 k + 4 j .. + 3 of k step k:
             // the order in which the codes of K come out of ldmatrix.
             const uint2* q = reinterpret_cast<const uint2*>(
@@ -453,7 +483,7 @@ struct PagedWarp {
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
             // 2^e >= the row's largest magnitude, e in [-125, 127].
             const int e = min(max((int)(a >> 23) - 126, -125), 127);
-            const float inv = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23) *
+            const float inv = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23 | p.qflip) *
                               (e == 127 ? 0.5f : 1.f);
             rowscale = p.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
@@ -469,8 +499,10 @@ struct PagedWarp {
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
-                    split_tf32(live ? __ldg(q + 8 * k + j + 4 * w) : 0.f, qa[k][w], qb[k][w]);
+                for (int w = 0; w < 2; ++w) {
+                    const float x = live ? __ldg(q + 8 * k + j + 4 * w) : 0.f;
+                    split_tf32(__uint_as_float(__float_as_uint(x) ^ p.qflip), qa[k][w], qb[k][w]);
+                }
         }
     }
 
@@ -480,47 +512,46 @@ struct PagedWarp {
         hi = *reinterpret_cast<const uint32_t*>(&h);
         lo = pack_f16(x - f.x, y - f.y);
     }
-    __device__ __forceinline__ static void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo,
-                                                      float& rx, float& ry) {
-        hi = pack_bf16(x, y);
-        const float dx = x - __uint_as_float(hi << 16), dy = y - __uint_as_float(hi & 0xffff0000u);
-        lo = pack_bf16(dx, dy);
-        rx = dx - __uint_as_float(lo << 16);
-        ry = dy - __uint_as_float(lo & 0xffff0000u);
+    // x and y become what hi and the residual leave.
+    __device__ __forceinline__ static uint32_t take_bf16(float& x, float& y) {
+        const uint32_t hi = pack_bf16(x, y);
+        x -= __uint_as_float(hi << 16);
+        y -= __uint_as_float(hi & 0xffff0000u);
+        return hi;
     }
+    // hi + lo = x to 22 bits, both rounded to nearest (the MMA ignores the
+    // low 13 bits of lo).
     __device__ __forceinline__ static void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-        hi = __float_as_uint(x) & 0xffffe000u;
-        lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+        hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
     }
 
-    // Shared-memory address of 16-byte chunk c of row r of a swizzled tile.
-    __device__ __forceinline__ static uint32_t chunk(uint32_t tile, int r, int c) {
-        if constexpr (C::SEGB == 128)
-            return tile + (uint32_t)((c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        else
-            return tile + (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    __device__ __forceinline__ static float lds(uint32_t addr) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+        return v;
     }
 
-    // One tile: `mask` bit t says whether token t counts (the rows of V of
-    // the others are zero), ks and vs are the tile's scales.
-    __device__ __forceinline__ void tile(const PagedParams& p, uint32_t k_smem, uint32_t v_smem,
-                                         unsigned mask, const float* ks, const float* vs,
-                                         int lane) {
-        const int row8 = lane & 7, mat = lane >> 3, j = lane & 3;
+    // One tile: bit t of `mask` says whether token t counts (the rows of V of
+    // the others are zero); ks and vs are the tile's scales.
+    __device__ __forceinline__ void tile(uint32_t stage, unsigned mask, const float* ks,
+                                         const float* vs, int lane) {
+        const int j = lane & 3;
         float s[4][4];
+        const uint32_t ka[2] = {stage + k_off, (stage + k_off) ^ 64u};
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-            const int r = 8 * n + row8;
 #pragma unroll
-            for (int c = 0; c < C::RB / 16; c += 4) {
+            for (int c = 0; c < CH; c += 4) {
                 uint32_t f[4];
-                ldsm_x4(chunk(k_smem, r, c + mat), f[0], f[1], f[2], f[3]);
-                if constexpr (T == kBf16) {
+                ldsm_x4(ka[(c >> 2) & 1] + (uint32_t)(n * 8 * C::SEGB + (c >> 3) * C::SEG_TILE),
+                        f[0], f[1], f[2], f[3]);
+                if constexpr (kB16) {
                     mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[0], f[1]);
                     mma_bf16_16816(s[n], qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, f[2], f[3]);
-                } else if constexpr (T == kE4m3) {
+                } else if constexpr (T == kPagesE4m3) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mma_f16_16816(s[n], qa[c + i][0], qb[c + i][0], qa[c + i][1], qb[c + i][1],
@@ -539,48 +570,61 @@ struct PagedWarp {
                 }
             }
         }
-        // Scores in the log2 domain; lane (r, j) holds head r, tokens
-        // 8 n + 2 j and + 1.
-        float x[4][2], vsc[4][2], mx = -INFINITY, vmax = 0.f;
+        // Lane (r, j) holds head r, tokens 8 n + 2 j and + 1.  x: scores, up
+        // to the factor `f` that makes them logarithms to base 2.
+        float x[4][2], vsc[4][2], vmax = 0.f, f = rowscale;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 4; ++n) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 8 * n + 2 * j + i;
-                const bool on = (mask >> t) & 1u;
-                float y = (kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i]) * rowscale;
-                if constexpr (T == kE4m3) {
-                    y *= ks[t];
-                    vsc[n][i] = on ? vs[t] : 0.f;
-                    vmax = fmaxf(vmax, fabsf(vsc[n][i]));
-                }
-                x[n][i] = on ? y : -INFINITY;
-                mx = fmaxf(mx, x[n][i]);
+            for (int i = 0; i < 2; ++i) x[n][i] = kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i];
+            if constexpr (T == kPagesE4m3) {
+                const float2 kk = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * j);
+                const float2 vv = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * j);
+                x[n][0] *= kk.x * rowscale;
+                x[n][1] *= kk.y * rowscale;
+                vsc[n][0] = vv.x;
+                vsc[n][1] = vv.y;
             }
+        }
+        if constexpr (T == kPagesE4m3) f = 1.f;
+        if (mask != 0xffffffffu) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!((mask >> (8 * n + 2 * j + i)) & 1u)) x[n][i] = -INFINITY, vsc[n][i] = 0.f;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) mx = fmaxf(mx, fmaxf(x[n][0], x[n][1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * f;
         const float m_new = fmaxf(m, mx);
         const float base = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m - base);  // 1 where the maximum stands
+        const float alpha = m == m_new ? 1.f : fast_exp2(m - base);
         float rescale = alpha, vinv = 1.f;
-        if constexpr (T == kE4m3) {
+        if constexpr (T == kPagesE4m3) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) vmax = fmaxf(vmax, fmaxf(fabsf(vsc[n][0]), fabsf(vsc[n][1])));
             vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
             vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-            // The power of two at or below the largest V scale so far.
+            // The power of two at or below the largest V scale so far; 1 /
+            // vexp by its exponent (halved where that is past the range).
             const float v2 = fmaxf(
                 vexp, __uint_as_float(min(__float_as_uint(vmax), 0x7f000000u) & 0x7f800000u));
-            rescale = alpha * (vexp / v2);
+            if (v2 != vexp) rescale = alpha * (vexp / v2);
             vexp = v2;
-            vinv = 1.f / v2;
+            const uint32_t e = __float_as_uint(v2);
+            vinv = e == 0x7f000000u ? 5.877471754e-39f : __uint_as_float(0x7f000000u - e);
         }
         float sum = 0.f;
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                x[n][i] = exp2f(x[n][i] - base);
+                x[n][i] = fast_exp2(fmaf(x[n][i], f, -base));
                 sum += x[n][i];
-                if constexpr (T == kE4m3) x[n][i] *= vsc[n][i] * vinv;
+                if constexpr (T == kPagesE4m3) x[n][i] *= vsc[n][i] * vinv;
             }
         m = m_new;
         l = l * alpha + sum;
@@ -591,52 +635,59 @@ struct PagedWarp {
                 for (int k = 0; k < 4; ++k) acc[i][k] *= rescale;
         }
         // O += P V.
-        if constexpr (T == kF32) {
+        const uint32_t v0 = stage + C::TILEB + v_off;
+        if constexpr (T == kPagesF32) {
+            // Rows 2 j and 2 j + 1 of a k step: the second is 128 bytes on,
+            // its chunks exchanged by the swizzle.
+            const uint32_t v1 = (v0 + 128u) ^ 16u;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {  // tokens 8 n ..: k step n
                 uint32_t h0, l0, h1, l1;
                 split_tf32(x[n][0], h0, l0);
                 split_tf32(x[n][1], h1, l1);
-                const int r0 = 8 * n + 2 * j;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const int d = 8 * i + (lane >> 2);
+                    const uint32_t add = (uint32_t)(n * 1024 + (i >> 2) * C::SEG_TILE);
+                    const uint32_t flip = (uint32_t)((2 * i & 7) << 4);
                     uint32_t a0, a1, b0, b1;
-                    split_tf32(lds(chunk(v_smem, r0, d >> 2) + (d & 3) * 4), a0, a1);
-                    split_tf32(lds(chunk(v_smem, r0 + 1, d >> 2) + (d & 3) * 4), b0, b1);
+                    split_tf32(lds((v0 ^ flip) + add), a0, a1);
+                    split_tf32(lds((v1 ^ flip) + add), b0, b1);
                     mma_tf32_1688(acc[i], h0, l0, h1, l1, a0, b0);
                     mma_tf32_1688(acc[i], h0, l0, h1, l1, a1, b1);
                 }
             }
         } else {
-            const bool third = T == kBf16 && !p.out_bf16;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {  // tokens 16 k ..
                 uint32_t a[4], c0 = 0, c1 = 0;
-                if constexpr (T == kE4m3) {
+                if constexpr (T == kPagesE4m3) {
                     split_f16(x[2 * k][0], x[2 * k][1], a[0], a[1]);
                     split_f16(x[2 * k + 1][0], x[2 * k + 1][1], a[2], a[3]);
                 } else {
-                    float r0, r1, r2, r3;
-                    split_bf16(x[2 * k][0], x[2 * k][1], a[0], a[1], r0, r1);
-                    split_bf16(x[2 * k + 1][0], x[2 * k + 1][1], a[2], a[3], r2, r3);
-                    c0 = pack_bf16(r0, r1);
-                    c1 = pack_bf16(r2, r3);
+                    a[0] = take_bf16(x[2 * k][0], x[2 * k][1]);
+                    a[1] = take_bf16(x[2 * k][0], x[2 * k][1]);
+                    a[2] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
+                    a[3] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
+                    if constexpr (T == kPagesBf16Wide) {
+                        c0 = take_bf16(x[2 * k][0], x[2 * k][1]);
+                        c1 = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
+                    }
                 }
                 // Matrices of one ldmatrix: tokens 0-7 and 8-15 of the step,
                 // chunks c and c + 1.
-                const int r = 16 * k + (mat & 1) * 8 + row8;
 #pragma unroll
-                for (int c = 0; c < C::RB / 16; c += 2) {
-                    uint32_t f[4];
-                    ldsm_x4_t(chunk(v_smem, r, c + (mat >> 1)), f[0], f[1], f[2], f[3]);
-                    if constexpr (T == kE4m3) {
+                for (int c = 0; c < CH; c += 2) {
+                    uint32_t f4[4];
+                    ldsm_x4_t((v0 ^ (uint32_t)((c & 7) << 4)) +
+                                  (uint32_t)(k * 16 * C::SEGB + (c >> 3) * C::SEG_TILE),
+                              f4[0], f4[1], f4[2], f4[3]);
+                    if constexpr (T == kPagesE4m3) {
                         // A code pair of one token per half word: split into
                         // the even and the odd column's tokens.
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
-                            const uint32_t g0 = __byte_perm(f[2 * w], 0u, 0x3120);
-                            const uint32_t g1 = __byte_perm(f[2 * w + 1], 0u, 0x3120);
+                            const uint32_t g0 = __byte_perm(f4[2 * w], 0u, 0x3120);
+                            const uint32_t g1 = __byte_perm(f4[2 * w + 1], 0u, 0x3120);
                             mma_f16_16816(acc[2 * (c + w)], a[0], a[1], a[2], a[3],
                                           e4m3x2_to_f16x2((uint16_t)g0),
                                           e4m3x2_to_f16x2((uint16_t)g1));
@@ -645,11 +696,11 @@ struct PagedWarp {
                                           e4m3x2_to_f16x2((uint16_t)(g1 >> 16)));
                         }
                     } else {
-                        mma_bf16_16816(acc[c], a[0], a[1], a[2], a[3], f[0], f[1]);
-                        mma_bf16_16816(acc[c + 1], a[0], a[1], a[2], a[3], f[2], f[3]);
-                        if (third) {
-                            mma_bf16_16816(acc[c], c0, 0u, c1, 0u, f[0], f[1]);
-                            mma_bf16_16816(acc[c + 1], c0, 0u, c1, 0u, f[2], f[3]);
+                        mma_bf16_16816(acc[c], a[0], a[1], a[2], a[3], f4[0], f4[1]);
+                        mma_bf16_16816(acc[c + 1], a[0], a[1], a[2], a[3], f4[2], f4[3]);
+                        if constexpr (T == kPagesBf16Wide) {
+                            mma_bf16_16816(acc[c], c0, 0u, c1, 0u, f4[0], f4[1]);
+                            mma_bf16_16816(acc[c + 1], c0, 0u, c1, 0u, f4[2], f4[3]);
                         }
                     }
                 }
@@ -657,27 +708,24 @@ struct PagedWarp {
         }
     }
 
-    __device__ __forceinline__ static float lds(uint32_t addr) {
-        float v;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-        return v;
-    }
-
-    // Calls f(column, value) for this lane's elements of its head's row.
+    // Calls f(column, value, value of column + 1) for this lane's elements of
+    // its head's row.
     template <typename F>
-    __device__ __forceinline__ void each(int lane, F f) const {
+    __device__ __forceinline__ void each2(int lane, F f) const {
         const int j = lane & 3;
 #pragma unroll
         for (int i = 0; i < NT; i += 2)
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float v = acc[i + w][k] + acc[i + w][k + 2];
-                    if constexpr (T == kE4m3) v *= vexp;
-                    const int col = T == kE4m3 ? 8 * i + 4 * j + 2 * k + w : 8 * (i + w) + 2 * j + k;
-                    f(col, v);
+            for (int k = 0; k < 2; ++k) {
+                if constexpr (T == kPagesE4m3) {
+                    // Tiles i and i + 1 hold the even and odd columns of 16.
+                    f(8 * i + 4 * j + 2 * k, (acc[i][k] + acc[i][k + 2]) * vexp,
+                      (acc[i + 1][k] + acc[i + 1][k + 2]) * vexp);
+                } else {
+                    f(8 * (i + k) + 2 * j, acc[i + k][0] + acc[i + k][2],
+                      acc[i + k][1] + acc[i + k][3]);
                 }
+            }
     }
 
     // The row sum of the exponentials over the quad's lanes.
@@ -695,16 +743,23 @@ struct PagedWarp {
             dst[kHeadRows + r] = s;
         }
         float* o = dst + 2 * kHeadRows + r * D;
-        each(lane, [&](int col, float v) { o[col] = v; });
+        each2(lane, [&](int col, float x, float y) {
+            *reinterpret_cast<float2*>(o + col) = make_float2(x, y);
+        });
     }
 
     __device__ __forceinline__ void write_out(const PagedParams& p, int b, int u, int lane) const {
         const float s = row_sum();
-        const int head = (u / p.blocks) * p.group + (u % p.blocks) * kHeadRows + (lane >> 2);
-        if ((u % p.blocks) * kHeadRows + (lane >> 2) >= p.group) return;
-        const long long at = (long long)b * p.hq + head;
-        if (p.lse && (lane & 3) == 0) p.lse[at] = paged_lse(m, s);
-        each(lane, [&](int col, float v) { paged_store(p, at * D + col, paged_ratio(v, s)); });
+        const int row = (u % p.blocks) * kHeadRows + (lane >> 2);
+        if (row < p.group) {
+            const long long at = (long long)b * p.hq + (u / p.blocks) * p.group + row;
+            const float inv = paged_inverse(s);
+            if (p.lse && (lane & 3) == 0) p.lse[at] = paged_lse(m, s);
+            each2(lane, [&](int col, float x, float y) {
+                paged_store2(p, at * D + col, x * inv, y * inv);
+            });
+        }
+        __syncwarp();
     }
 };
 
@@ -716,109 +771,99 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(pd_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::kOffPiece);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
-
-    // Padded rows of the batch, and lengths out of range.
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-        const int len = __ldg(p.lens + b);
-        if ((len < 0 || len > p.cap) && threadIdx.x == 0) atomicOr(p.ctr + kCtrError, kErrSeqLen);
-        if (len > 0) continue;
-        for (int i = threadIdx.x; i < p.hq * D; i += C::kThreads)
-            paged_store(p, (long long)b * p.hq * D + i, 0.f);
-        for (int i = threadIdx.x; p.lse && i < p.hq; i += C::kThreads)
-            p.lse[(long long)b * p.hq + i] = -INFINITY;
+    unsigned char* ring = smem + warp * C::ST * C::STAGEB;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::ST;
+    int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * C::ST;
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * kTile;
+    float* deposit0 = p.heads + ((long long)blockIdx.x * C::NW + warp) * C::PART;
+    const int units = p.hkv * p.blocks;
+    // A warp's barriers are its own: no other warp has to see them.
+    if (lane == 0) {
+        for (int s = 0; s < C::ST; ++s) mbar_init(full + s, T == kPagesE4m3 ? 33 : 1);
+        fence_barrier_init();
+        prefetch_tmap(&p.tk);
+        prefetch_tmap(&p.tv);
     }
+    __syncwarp();
+    // Launched while the kernel ahead on the stream may still run: nothing is
+    // read or written before it has completed, and only then may the next
+    // one be launched (so whatever it reads early is older than that).
+    pdl_wait_prerequisite();
+    pdl_launch_dependents();
 
     const long long total = paged_total(p);
-    if (total == 0) return;
     const long long workers = min((long long)gridDim.x * C::NW, total);
-    if ((long long)blockIdx.x * C::NW >= workers) return;
     const long long w = (long long)blockIdx.x * C::NW + warp;
     const long long x0 = w < workers ? share_begin(total, workers, w) : 0;
     const int tiles = w < workers ? (int)(share_begin(total, workers, w + 1) - x0) : 0;
+    PagedPiece head{}, tail{};
 
-    if (lane == 0) {
-        for (int s = 0; s < C::ST; ++s) mbar_init(bars + warp * C::ST + s, T == kE4m3 ? 33 : 1);
-        fence_barrier_init();
-    }
-    if (threadIdx.x == 0) misc[0] = 0;
-    __syncthreads();
-
-    unsigned char* ring = smem + warp * C::ST * C::STAGEB;
-    uint64_t* full = bars + warp * C::ST;
-    int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * C::ST;
-    float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * kTile;
-    float* deposit0 = reinterpret_cast<float*>(smem + C::kOffDeposit) + warp * C::PART;
-    const int units = p.hkv * p.blocks;
+    // Padded rows of the batch, and lengths out of range.
+    auto empty_rows = [&]() {
+        for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+            const int len = __ldg(p.lens + b);
+            if ((len < 0 || len > p.cap) && threadIdx.x == 0)
+                atomicOr(p.ctr + kCtrError, kErrSeqLen);
+            if (len > 0) continue;
+            for (int i = 2 * threadIdx.x; i < p.hq * D; i += 2 * C::kThreads)
+                paged_store2(p, (long long)b * p.hq * D + i, 0.f, 0.f);
+            for (int i = threadIdx.x; p.lse && i < p.hq; i += C::kThreads)
+                p.lse[(long long)b * p.hq + i] = -INFINITY;
+        }
+    };
 
     if (tiles > 0) {
         PagedPos pos = paged_find(p, x0);
-        {
-            const PagedPos end = paged_find(p, x0 + tiles - 1);
-            if (lane == 0) {
-                PagedPiece head{}, tail{};
-                tail.b = end.b, tail.u = end.u, tail.n = end.s.n;
-                if (end.b == pos.b && end.u == pos.u) {
-                    if (pos.i > 0 || end.i + 1 < end.s.n) tail.lo = pos.i, tail.hi = end.i + 1;
-                } else {
-                    if (pos.i > 0)
-                        head.b = pos.b, head.u = pos.u, head.lo = pos.i, head.hi = head.n = pos.s.n;
-                    if (end.i + 1 < end.s.n) tail.lo = 0, tail.hi = end.i + 1;
-                }
-                pieces[2 * warp] = head;
-                pieces[2 * warp + 1] = tail;
-            }
-        }
-        const uint64_t pol = l2_evict_first_policy();
+        const PagedPos start = pos;
+        const uint64_t pol = p.blocks == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
         // A box is `box` rows of one 128-byte column segment of K or V; the
         // boxes of a tile are spread over the lanes: lane = sub-box +
         // boxes-down * (segment, K or V).
         const int down = kTile / p.box;
         const int sub = lane & (down - 1), first = lane / down, step = kTile / down;
-        int page = 0;  // of this lane's sub-box in the next tile to be issued
-        auto token0 = [&](const PagedPos& q) {
-            return (q.i < q.s.a ? q.i : q.i + q.s.f - q.s.a) * kTile;
-        };
+        const int from = lane / p.box, rem = lane % p.box;
+        int page = 0;    // of this lane's sub-box in the next tile to be issued
+        int in_page = 0;
+        int t0 = 0;      // that tile's first token
         auto fetch_page = [&]() {
-            const int t = token0(pos) + sub * p.box;
-            if (t < pos.s.len)
-                page = __ldg(p.table + (long long)pos.b * p.max_pages + t / p.page_size);
+            t0 = (pos.i < pos.s.a ? pos.i : pos.i + pos.s.f - pos.s.a) * kTile;
+            const int t = t0 + sub * p.box;
+            const int entry = (int)(__umulhi((unsigned)t, p.page_mul) >> p.page_shift);
+            in_page = t - entry * p.page_size;
+            if (t < pos.s.len) page = __ldg(p.table + (long long)pos.b * p.max_pages + entry);
         };
         auto issue = [&](int slot) {
-            const int t0 = token0(pos);
-            const int boxes = min(down, (pos.s.len - t0 + p.box - 1) / p.box);
-            int pg = page;
-            if (sub < boxes && (pg < 0 || pg >= p.n_pages)) {
-                atomicOr(p.ctr + kCtrError, kErrPage);
-                pg = 0;
-            }
-            const int t = t0 + sub * p.box;
-            const int in_page = t % p.page_size;
-            const int h = pos.u / p.blocks;
+            const int left = pos.s.len - t0;  // tokens from here on
+            const bool mine = sub * p.box < left;
+            const int h = p.blocks == 1 ? pos.u : pos.u / p.blocks;
             unsigned char* stage = ring + slot * C::STAGEB;
             if (lane == 0) {
+                const int boxes = left >= kTile ? down : (left + p.box - 1) / p.box;
                 meta[slot] = make_int4(pos.b, pos.u, pos.i, t0);
                 mbar_arrive_expect_tx(full + slot, (uint32_t)(boxes * p.box * 2 * C::RB));
             }
             __syncwarp();
-            if (sub < boxes) {
+            if (mine) {
+                if ((unsigned)page >= (unsigned)p.n_pages) {
+                    atomicOr(p.ctr + kCtrError, kErrPage);
+                    page = 0;
+                }
                 for (int c = first; c < 2 * C::SEGS; c += step) {
                     const int v = c & 1, seg = c >> 1;
-                    tma_load_4d(stage + v * C::TILEB + seg * kTile * C::SEGB +
-                                    sub * p.box * C::SEGB,
-                                v ? &p.tv : &p.tk, seg * (C::SEGB / C::ES), in_page, h, pg,
+                    tma_load_4d(stage + v * C::TILEB + seg * C::SEG_TILE + sub * p.box * C::SEGB,
+                                v ? &p.tv : &p.tk, seg * (C::SEGB / C::ES), in_page, h, page,
                                 full + slot, pol);
                 }
             }
-            if constexpr (T == kE4m3) {
+            if constexpr (T == kPagesE4m3) {
                 // Lane = token: its scales, and its arrival once they landed.
-                const int mine = lane / p.box;
-                const int pg_t = __shfl_sync(0xffffffffu, pg, mine);
-                const int in_t = __shfl_sync(0xffffffffu, in_page, mine) + lane % p.box;
-                if (t0 + lane < pos.s.len) {
-                    const long long at = ((long long)pg_t * p.hkv + h) * p.page_size + in_t;
+                __syncwarp();
+                const int pg = __shfl_sync(0xffffffffu, page, from);
+                const int in = __shfl_sync(0xffffffffu, in_page, from) + rem;
+                if (lane < left) {
+                    const long long at = ((long long)pg * p.hkv + h) * p.page_size + in;
                     cp_async_4(scales + slot * 2 * kTile + lane, p.ks + at);
                     cp_async_4(scales + slot * 2 * kTile + kTile + lane, p.vs + at);
                 }
@@ -843,55 +888,77 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
         for (; issued < min(C::ST, tiles); ++issued) issue(issued);
 
         PagedWarp<T, D> state;
-        PagedSeq s{};
-        int done = 0;
+        state.init(lane);
+        state.reset();
+        state.load_q(p, start.b, start.u, lane);
+        PagedSeq s = start.s;
+        {
+            // What this warp leaves to be joined.
+            const PagedPos end = paged_find(p, x0 + tiles - 1);
+            tail.b = end.b, tail.u = end.u, tail.n = end.s.n;
+            if (end.b == start.b && end.u == start.u) {
+                if (start.i > 0 || end.i + 1 < end.s.n) tail.lo = start.i, tail.hi = end.i + 1;
+            } else {
+                if (start.i > 0) {
+                    head.b = start.b, head.u = start.u, head.lo = start.i;
+                    head.hi = head.n = start.s.n;
+                }
+                if (end.i + 1 < end.s.n) tail.hi = end.i + 1;
+            }
+        }
+        empty_rows();
+        int done = 0, slot = 0;
+        uint32_t parity = 0;
         bool lost = false, have0 = false, have1 = false;
         for (; done < tiles; ++done) {
-            const int slot = done % C::ST;
             // Bounded wait for the fill.
-            uint64_t since = 0;
-            for (uint32_t it = 0; !lost; ++it) {
-                if (__all_sync(0xffffffffu, mbar_try_wait(full + slot, (done / C::ST) & 1))) break;
-                if ((it & 31) == 31) {
-                    const uint64_t now = __shfl_sync(0xffffffffu, global_ns(), 0);
-                    if (since == 0) since = now;
-                    lost = now - since > p.timeout_ns;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(full + slot, parity))) {
+                const uint64_t since = global_ns();
+                for (uint32_t it = 1;
+                     !__all_sync(0xffffffffu, mbar_try_wait(full + slot, parity)); ++it) {
+                    if ((it & 31) == 0 &&
+                        __any_sync(0xffffffffu, global_ns() - since > p.timeout_ns)) {
+                        lost = true;
+                        break;
+                    }
                 }
+                if (lost) break;
             }
-            if (lost) break;
             const int4 at = meta[slot];
-            if (done == 0 || at.z == 0) {
+            if (at.z == 0 && done > 0) {
                 s = paged_seq(p, __ldg(p.lens + at.x));
                 state.reset();
                 state.load_q(p, at.x, at.y, lane);
             }
             // Tokens of the set: bit t of the mask.
             const int t = at.w + lane;
-            const bool on = t < s.len &&
-                            (p.S + p.W == 0 || t < p.S || t >= s.len - p.W);
+            const bool on = t < s.len && (p.S + p.W == 0 || t < p.S || t >= s.len - p.W);
             const unsigned mask = __ballot_sync(0xffffffffu, on);
-            const uint32_t k_smem = smem_addr(ring + slot * C::STAGEB);
-            const uint32_t v_smem = k_smem + C::TILEB;
+            unsigned char* stage = ring + slot * C::STAGEB;
             if (mask != 0xffffffffu) {
                 // Rows of V that do not count may hold anything: zeros, so
                 // that 0 * NaN does not reach the sums.
                 if (!on) {
-                    unsigned char* v = ring + slot * C::STAGEB + C::TILEB + lane * C::SEGB;
                     for (int g = 0; g < C::SEGS; ++g)
-                        for (int c = 0; c < C::SEGB / 16; ++c)
-                            *reinterpret_cast<uint4*>(v + g * kTile * C::SEGB + c * 16) =
+                        for (int c = 0; c < C::SEGB; c += 16)
+                            *reinterpret_cast<uint4*>(stage + C::TILEB + g * C::SEG_TILE +
+                                                      lane * C::SEGB + c) =
                                 make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
             }
             const float* sc = scales + slot * 2 * kTile;
-            state.tile(p, k_smem, v_smem, mask, sc, sc + kTile, lane);
+            state.tile(smem_addr(stage), mask, sc, sc + kTile, lane);
             __syncwarp();
             const bool last = done + 1 == tiles;
             if (issued < tiles) {
                 issue(slot);
                 ++issued;
+            }
+            if (++slot == C::ST) {
+                slot = 0;
+                parity ^= 1u;
             }
             if (last || at.z + 1 == s.n) {
                 const bool whole = done >= at.z && at.z + 1 == s.n;
@@ -909,27 +976,31 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
         if (lost) {
             // Nothing more is asked for; let what was asked for land (bounded).
             if (lane == 0) atomicOr(p.ctr + kCtrError, kErrTimeout);
-            for (int n = done; n < issued; ++n) {
-                const uint64_t t0 = global_ns();
-                while (!mbar_try_wait(full + n % C::ST, (n / C::ST) & 1))
-                    if (global_ns() - t0 > p.timeout_ns) break;
-            }
+            const uint64_t since = global_ns();
+            for (int n = done; n < issued; ++n)
+                while (!mbar_try_wait(full + n % C::ST, (uint32_t)(n / C::ST) & 1u))
+                    if (global_ns() - since > p.timeout_ns) break;
             __syncwarp();
             // Empty partials, so that the joins stay complete.
             state.reset();
             if (!have0) state.deposit(deposit0, lane);
             if (!have1) state.deposit(reinterpret_cast<float*>(ring), lane);
         }
-    } else if (lane == 0) {
-        pieces[2 * warp] = PagedPiece{};
-        pieces[2 * warp + 1] = PagedPiece{};
+    } else {
+        empty_rows();
+    }
+    if ((long long)blockIdx.x * C::NW >= workers) return;
+    if (lane == 0) {
+        pieces[2 * warp] = head;
+        pieces[2 * warp + 1] = tail;
     }
     __syncthreads();
 
-    // Join what spans warps: runs of pieces of one (sequence, unit).
+    // Join what spans warps: runs of pieces of one (sequence, unit).  Piece 2 i
+    // is warp i's first run, piece 2 i + 1 its last.
     auto partial = [&](int i) {
         return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * C::ST * C::STAGEB)
-                       : reinterpret_cast<const float*>(smem + C::kOffDeposit) + (i >> 1) * C::PART;
+                       : p.heads + ((long long)blockIdx.x * C::NW + (i >> 1)) * C::PART;
     };
     for (int i = 0; i < 2 * C::NW;) {
         const PagedPiece a = pieces[i];
@@ -938,10 +1009,12 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
             continue;
         }
         int k = i, hi = 0;
+        unsigned there = 0;
         for (; k < 2 * C::NW; ++k) {
             if (pieces[k].hi == 0) continue;
             if (pieces[k].b != a.b || pieces[k].u != a.u) break;
             hi = pieces[k].hi;
+            there |= 1u << k;
         }
         const bool whole = a.lo == 0 && hi == a.n;
         const int rows = min(kHeadRows, p.group - (a.u % p.blocks) * kHeadRows);
@@ -950,24 +1023,27 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
         // A run that began in an earlier CTA is this CTA's first partial, one
         // that goes on in the next its second.
         float* mine = p.part + ((long long)blockIdx.x * 2 + (a.lo == 0 ? 1 : 0)) * C::PART;
-        for (int e = threadIdx.x; e < rows * D; e += C::kThreads) {
+        for (int e = 4 * threadIdx.x; e < rows * D; e += 4 * C::kThreads) {
             const int r = e / D;
             float M = -INFINITY;
-            for (int n = i; n < k; ++n)
-                if (pieces[n].hi) M = fmaxf(M, partial(n)[r]);
-            float o = 0.f, l = 0.f;
-            for (int n = i; n < k; ++n) {
-                if (!pieces[n].hi) continue;
-                const float* q = partial(n);
+            for (unsigned left = there; left; left &= left - 1)
+                M = fmaxf(M, partial(__ffs(left) - 1)[r]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+            for (unsigned left = there; left; left &= left - 1) {
+                const float* q = partial(__ffs(left) - 1);
                 const float f = merge_weight(q[r], M);
-                o += q[2 * kHeadRows + e] * f;
+                const float4 v = *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e);
+                o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
                 l += q[kHeadRows + r] * f;
             }
             if (whole) {
-                paged_store(p, head0 * D + e, paged_ratio(o, l));
+                const float inv = paged_inverse(l);
+                paged_store2(p, head0 * D + e, o.x * inv, o.y * inv);
+                paged_store2(p, head0 * D + e + 2, o.z * inv, o.w * inv);
                 if (p.lse && e % D == 0) p.lse[head0 + r] = paged_lse(M, l);
             } else {
-                __stcg(mine + 2 * kHeadRows + e, o);
+                __stcg(reinterpret_cast<float4*>(mine + 2 * kHeadRows + e), o);
                 if (e % D == 0) {
                     __stcg(mine + r, M);
                     __stcg(mine + kHeadRows + r, l);
@@ -976,43 +1052,48 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
         }
         if (!whole) {
             // The last CTA of this (sequence, unit) to arrive joins it.
-            __syncthreads();
             if (threadIdx.x == 0) {
                 // Tile 0 of the run in the numbering, from one of its tiles.
-                const int at = i >> 1;
-                const long long begin =
-                    share_begin(total, workers, (long long)blockIdx.x * C::NW + at) +
-                    ((i & 1) && pieces[i].lo == 0
-                         ? share_begin(total, workers, (long long)blockIdx.x * C::NW + at + 1) -
-                               share_begin(total, workers, (long long)blockIdx.x * C::NW + at) -
-                               pieces[i].hi
-                         : 0) -
-                    pieces[i].lo;
-                const int c0 = (int)(share_of(total, workers, begin) / C::NW);
-                const int c1 = (int)(share_of(total, workers, begin + a.n - 1) / C::NW);
-                __threadfence();
+                const long long wi = (long long)blockIdx.x * C::NW + (i >> 1);
+                const long long begin = (i & 1) && a.lo == 0
+                                            ? share_begin(total, workers, wi + 1) - a.hi
+                                            : share_begin(total, workers, wi) - a.lo;
+                misc[2] = (int)(share_of(total, workers, begin) / C::NW);
+                misc[3] = (int)(share_of(total, workers, begin + a.n - 1) / C::NW);
+            }
+            __syncthreads();
+            const int c0 = misc[2], c1 = misc[3];
+            if (threadIdx.x == 0) {
+                // Releases what the CTA wrote before the barrier, and takes
+                // what the others released.
                 const unsigned old = atom_add_acq_rel_gpu(p.ctr + kPagedTickets + c0, 1u);
                 misc[1] = old == (unsigned)(c1 - c0) ? 1 : 0;
-                misc[2] = c0;
-                misc[3] = c1;
                 if (old == (unsigned)(c1 - c0)) p.ctr[kPagedTickets + c0] = 0u;
-                __threadfence();
             }
             __syncthreads();
             if (misc[1]) {
-                const int c0 = misc[2], c1 = misc[3];
-                for (int e = threadIdx.x; e < rows * D; e += C::kThreads) {
+                for (int e = 4 * threadIdx.x; e < rows * D; e += 4 * C::kThreads) {
                     const int r = e / D;
-                    float M = -INFINITY, o = 0.f, l = 0.f;
-                    for (int c = c0; c <= c1; ++c)
-                        M = fmaxf(M, __ldcg(p.part + ((long long)c * 2 + (c == c0)) * C::PART + r));
+                    auto slot = [&](int c) {
+                        return p.part + ((long long)c * 2 + (c == c0)) * C::PART;
+                    };
+                    float M = -INFINITY;
+#pragma unroll 8
+                    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot(c) + r));
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float l = 0.f;
+#pragma unroll 8
                     for (int c = c0; c <= c1; ++c) {
-                        const float* q = p.part + ((long long)c * 2 + (c == c0)) * C::PART;
+                        const float* q = slot(c);
                         const float f = merge_weight(__ldcg(q + r), M);
-                        o += __ldcg(q + 2 * kHeadRows + e) * f;
+                        const float4 v = __ldcg(
+                            reinterpret_cast<const float4*>(q + 2 * kHeadRows + e));
+                        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
                         l += __ldcg(q + kHeadRows + r) * f;
                     }
-                    paged_store(p, head0 * D + e, paged_ratio(o, l));
+                    const float inv = paged_inverse(l);
+                    paged_store2(p, head0 * D + e, o.x * inv, o.y * inv);
+                    paged_store2(p, head0 * D + e + 2, o.z * inv, o.w * inv);
                     if (p.lse && e % D == 0) p.lse[head0 + r] = paged_lse(M, l);
                 }
             }
