@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "alspec.h"
 #include "host.h"
@@ -14,22 +15,81 @@
 namespace alspec {
 namespace {
 
-// A 2-D bf16 matrix [rows][k] with rows `stride` elements apart; boxes of 64
-// columns x `box` rows with 128-byte swizzle.
-alspec_status encode_matrix(CUtensorMap* map, const void* base, int k, int rows, int64_t stride,
-                            int box) {
+// Views of a bf16 matrix [rows][k] with rows `stride` elements apart, boxes
+// of `box` rows with 128-byte swizzle: `whole` as 64-column blocks, `group`
+// of them in a box, and `end` as plain columns.
+alspec_status encode_matrix(CUtensorMap* whole, CUtensorMap* end, const void* base, int k, int rows,
+                            int64_t stride, int box, int group) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     const alspec_status st = tiled_map_encoder(&encode);
     if (st != ALSPEC_OK) return st;
-    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t boxes[2] = {kLinK, (cuuint32_t)box};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r =
-        encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-               boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? ALSPEC_OK : ALSPEC_ERR_INVALID_ARG;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    for (int w = 0; w < 2; ++w) {
+        CUtensorMap* map = w ? whole : end;
+        if (w && k < kLinK) continue;
+        const cuuint64_t dims[3] = {(cuuint64_t)(w ? kLinK : k), (cuuint64_t)rows,
+                                    (cuuint64_t)(k / kLinK)};
+        const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, kLinK * 2};
+        const cuuint32_t boxes[3] = {kLinK, (cuuint32_t)box, (cuuint32_t)group};
+        const CUresult r =
+            encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w ? 3 : 2, const_cast<void*>(base), dims,
+                   strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return ALSPEC_ERR_INVALID_ARG;
+    }
+    if (k < kLinK) *whole = *end;  // no whole block: never used
+    return ALSPEC_OK;
+}
+
+// Clusters of `c` CTAs of the kernel that the current device holds at once
+// (asked once).
+int g_clusters[kMaxDevices][kLinMaxSplit + 1] = {};
+std::mutex g_clusters_mutex;
+
+bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
+    int dev = 0;
+    if (!ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return false;
+    if (smem_attr_once(reinterpret_cast<const void*>(linear_kernel), kLinRing + 1024) != ALSPEC_OK)
+        return false;
+    std::lock_guard<std::mutex> lock(g_clusters_mutex);
+    int(&n)[kLinMaxSplit + 1] = g_clusters[dev];
+    for (int c = 1; c <= kLinMaxSplit && n[kLinMaxSplit] == 0; ++c) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)c);
+        cfg.blockDim = dim3(kLinThreads);
+        cfg.dynamicSmemBytes = kLinRing + 1024;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = c;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (!ok(cudaOccupancyMaxActiveClusters(&n[c], linear_kernel, &cfg)) || n[c] < 1) {
+            n[kLinMaxSplit] = 0;
+            return false;
+        }
+    }
+    for (int c = 0; c <= kLinMaxSplit; ++c) out[c] = n[c];
+    return true;
+}
+
+// CTAs that share the K of a tile: the number that makes (waves of clusters)
+// x (blocks of a CTA, plus four for the exchange where there is one)
+// smallest.  Clusters leave SMs idle (148 SMs hold 74 pairs, but 45 clusters
+// of 3, 33 of 4, 15 of 7 or 8), and a second wave costs more than an idle SM:
+// 33 x 4096 x 6144 (48 tiles) takes 24 us with 3 and 15.0 with 2.
+int choose_split(int64_t tiles, int kblocks) {
+    int n[kLinMaxSplit + 1];
+    if (!resident_clusters(n)) return 0;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int c = 1; c <= kLinMaxSplit && c <= std::max(1, kblocks / 4); ++c) {
+        const int64_t waves = (tiles + n[c] - 1) / n[c];
+        const int64_t cost = waves * ((kblocks + c - 1) / c + (c > 1 ? 4 : 0));
+        if (cost < least) least = cost, best = c;
+    }
+    return best;
 }
 
 }  // namespace
@@ -62,21 +122,26 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     p.row_tiles = (rows - 1) / p.nt + 1;
     const int64_t tiles = ((int64_t)n + kLinM - 1) / kLinM * p.row_tiles;
     p.kblocks = (k - 1) / kLinK + 1;
-    // K is split over a cluster while that finds idle SMs, at least four
-    // 64-column slices a CTA.
-    const int sms = sm_count_for_plan();
-    p.split = (int)std::max<int64_t>(
-        1, std::min<int64_t>({8, sms / std::max<int64_t>(tiles, 1), p.kblocks / 4}));
+    p.whole = k / kLinK;
+    p.split = choose_split(tiles, p.kblocks);
+    if (p.split == 0) return ALSPEC_ERR_CUDA;
     if (tiles * p.split > 0x7fffffff || n > 0x7fffffff - kLinM) return ALSPEC_ERR_UNSUPPORTED;
-    const int stage = (kLinM + p.nt) * 128;
-    p.stages = std::min({kLinMaxStages, kLinRing / stage,
-                         std::max(2, (p.kblocks + p.split - 1) / p.split)});
+    // Blocks of a stage: four (512 consecutive bytes of a row of W) where the
+    // ring holds two such stages, else two.  DRAM wants neighbouring columns
+    // asked for together: one block a stage, the ring as large, took 35.1 us
+    // for 16 x 8192 x 8192, two 26.4, four 26.9; for 33 x 4096 x 6144 two 16.0,
+    // four 15.0.
+    p.group = (kLinM + p.nt) * 128 * 8 <= kLinRing ? 4 : 2;
+    const int stage = (kLinM + p.nt) * 128 * p.group;
+    const int fills = ((p.kblocks + p.split - 1) / p.split + p.group - 1) / p.group;
+    p.stages = std::min({kLinMaxStages, kLinRing / stage, std::max(2, fills)});
     p.tmem_cols = 32;
     while (p.tmem_cols < p.nt) p.tmem_cols *= 2;
     const int smem = std::max({p.stages * stage, p.nt * kLinM * 4, kLinMinSmem}) + 1024;
-    alspec_status st = encode_matrix(&p.tw, w, k, n, k, kLinM);
+    alspec_status st = encode_matrix(&p.tw, &p.tw_end, w, k, n, k, kLinM, p.group);
     if (st != ALSPEC_OK) return st;
-    if ((st = encode_matrix(&p.tx, x, k, rows, x_stride ? x_stride : k, p.nt)) != ALSPEC_OK)
+    if ((st = encode_matrix(&p.tx, &p.tx_end, x, k, rows, x_stride ? x_stride : k, p.nt,
+                            p.group)) != ALSPEC_OK)
         return st;
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.residual = residual;

@@ -29,18 +29,24 @@ constexpr int kLinK = 64;         // columns of a stage: 128 bytes
 constexpr int kLinMaxN = 256;     // batch rows per tile
 constexpr int kLinMaxStages = 12;
 constexpr int kLinRing = 200 * 1024;
+constexpr int kLinMaxSplit = 8;   // CTAs of a cluster
+constexpr int kLinAhead = 4;      // stages asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM
 // holds one CTA and its TMEM allocation never waits for another's.
 constexpr int kLinMinSmem = 120 * 1024;
 
 struct LinearParams {
-    CUtensorMap tw, tx;  // 2-D: (k, row)
+    // Views of W and x: 3-D (column in a block, row, whole 64-column block),
+    // boxes of `group` blocks; and 2-D (column, row) for a last block of
+    // fewer columns, filled up with zeros.
+    CUtensorMap tw, tx, tw_end, tx_end;
     const __nv_bfloat16* bias;
     const void* residual;
     void* y;
-    int rows, n, kblocks;
+    int rows, n, kblocks, whole;  // 64-column blocks of k, and those without a fill
     int nt;        // batch rows per tile: a multiple of 16
     int row_tiles, split, stages;
+    int group;     // 64-column blocks a stage holds
     int tmem_cols;
     int out_bf16, act;
     unsigned* err;
@@ -172,7 +178,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     const int n0 = tile / p.row_tiles * kLinM, r0 = tile % p.row_tiles * p.nt;
     const int kb0 = (int)((long long)rank * p.kblocks / p.split);
     const int kb1 = (int)((long long)(rank + 1) * p.kblocks / p.split);
-    const int stage_bytes = kLinM * 128 + p.nt * 128;
+    const int stage_bytes = (kLinM + p.nt) * 128 * p.group;
+    const int fills = (kb1 - kb0 + p.group - 1) / p.group;
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -184,6 +191,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         fence_barrier_init();
         prefetch_tmap(&p.tw);
         prefetch_tmap(&p.tx);
+        prefetch_tmap(&p.tw_end);
+        prefetch_tmap(&p.tx_end);
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -199,20 +208,41 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     // Launched while the kernel ahead on the stream may still run: nothing is
     // read or written before it has completed, and only then may the next
     // one be launched.
+    // (W's first stages are asked for in L2 meanwhile, which is coherent
+    // whoever writes them: 16 x 8192 x 8192 back to back 25.9 -> 24.5 us.)
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < min(kLinAhead, fills); ++i) {
+            const int kb = kb0 + i * p.group;
+            if (kb + p.group <= min(kb1, p.whole)) tma_prefetch_3d(&p.tw, 0, n0, kb);
+        }
+    }
     pdl_wait_prerequisite();
     pdl_launch_dependents();
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
-            int i = 0;
-            for (int kb = kb0; kb < kb1; ++kb, ++i) {
+            const uint64_t keep = l2_evict_normal_policy();
+            const uint64_t policy = p.row_tiles == 1 ? l2_evict_first_policy() : keep;
+            for (int i = 0; i < fills; ++i) {
                 const int s = i % p.stages;
                 if (i >= p.stages && !lin_wait(empty + s, (i / p.stages - 1) & 1, abort, p)) break;
+                const int kb = kb0 + i * p.group;
                 unsigned char* w = ring + s * stage_bytes;
-                mbar_arrive_expect_tx(full + s, (uint32_t)stage_bytes);
-                tma_load_2d(w, &p.tw, kb * kLinK, n0, full + s, p.row_tiles == 1 ? once : keep);
-                tma_load_2d(w + kLinM * 128, &p.tx, kb * kLinK, r0, full + s, keep);
+                unsigned char* x = w + p.group * kLinM * 128;
+                if (kb + p.group <= min(kb1, p.whole)) {
+                    mbar_arrive_expect_tx(full + s, (uint32_t)stage_bytes);
+                    tma_load_3d(w, &p.tw, 0, n0, kb, full + s, policy);
+                    tma_load_3d(x, &p.tx, 0, r0, kb, full + s, keep);
+                } else {  // the last blocks of this CTA, one at a time
+                    const int blocks = min(p.group, kb1 - kb);
+                    mbar_arrive_expect_tx(full + s, (uint32_t)(blocks * (kLinM + p.nt) * 128));
+                    for (int g = 0; g < blocks; ++g) {
+                        tma_load_2d(w + g * kLinM * 128, &p.tw_end, (kb + g) * kLinK, n0, full + s,
+                                    policy);
+                        tma_load_2d(x + g * p.nt * 128, &p.tx_end, (kb + g) * kLinK, r0, full + s,
+                                    keep);
+                    }
+                }
             }
         }
     } else if (warp == 1) {
@@ -220,22 +250,26 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
             // fp32 accumulator, bf16 operands, both K-major.
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                    ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(kLinM >> 4) << 24);
-            for (int i = 0; i < kb1 - kb0; ++i) {
+            for (int i = 0; i < fills; ++i) {
                 const int s = i % p.stages;
                 if (!lin_wait(full + s, (i / p.stages) & 1, abort, p)) {
                     // Given up: let the copies in flight land (bounded).
                     const uint64_t t0 = global_ns();
-                    for (int j = i; j < min(i + p.stages, kb1 - kb0); ++j)
+                    for (int j = i; j < min(i + p.stages, fills); ++j)
                         while (!mbar_try_wait(full + j % p.stages, (j / p.stages) & 1))
                             if (global_ns() - t0 > p.timeout_ns) break;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t a = smem_addr(ring + s * stage_bytes);
-                const uint64_t da = lin_desc(a), db = lin_desc(a + kLinM * 128);
+                const int blocks = min(p.group, kb1 - kb0 - i * p.group);
+                for (int g = 0; g < blocks; ++g) {
+                    const uint64_t da = lin_desc(a + g * kLinM * 128);
+                    const uint64_t db = lin_desc(a + p.group * kLinM * 128 + g * p.nt * 128);
 #pragma unroll
-                for (int k = 0; k < kLinK / 16; ++k)  // 32 bytes of every row a step
-                    lin_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
+                    for (int k = 0; k < kLinK / 16; ++k)  // 32 bytes of every row a step
+                        lin_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || g > 0 || k > 0);
+                }
                 lin_commit(empty + s);
             }
             lin_commit(&done);

@@ -6,7 +6,7 @@ import torch
 
 from . import alspec as _c
 from .alspec import AlspecError
-from .paged import _On, _stream, _want
+from .paged import _CODES, _FLOATS, _on, _stream, _take_error, _want
 
 
 class Linear:
@@ -30,44 +30,44 @@ class Linear:
         self.weight, self.bias, self.device = weight, bias, weight.device
         self.n, self.k = weight.shape
         self.activation = _c.ACTIVATIONS[activation]
-        with _On(self.device):
-            self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._index = self.device.index
 
     def apply(self, x, residual=None, out=None, out_dtype=torch.bfloat16, stream=None):
         """x bf16 [rows, k] (rows may be slices of wider ones); residual, if
         given, and out are contiguous [rows, n] tensors of one type (fp32 or
         bf16; ``out_dtype`` where out is to be made) and may be the same
         tensor.  Returns out."""
-        dev = self.device
+        dev, n = self.device, self.n
         rows = x.shape[0]
-        _want(x.dim() == 2 and x.shape[1] == self.k and x.dtype is torch.bfloat16
-              and x.device == dev and x.stride(1) == 1,
-              f"x: a bf16 tensor [rows, {self.k}] on {dev} with consecutive columns is needed")
+        xt = x.stride()
+        if not (x.shape == (rows, self.k) and x.dtype is torch.bfloat16 and x.device == dev
+                and xt[1] == 1):
+            raise ValueError(f"x: a bf16 tensor [rows, {self.k}] on {dev} with consecutive "
+                             f"columns is needed, got {x.dtype} {tuple(x.shape)} on {x.device}")
         if out is None:
-            out = torch.empty((rows, self.n), device=dev,
+            out = torch.empty((rows, n), device=dev,
                               dtype=out_dtype if residual is None else residual.dtype)
-        for name, t in (("out", out), ("residual", residual)):
-            _want(t is None or (tuple(t.shape) == (rows, self.n) and t.device == dev
-                                and t.dtype in (torch.float32, torch.bfloat16)
-                                and t.dtype is out.dtype and t.is_contiguous()),
-                  f"{name}: a contiguous tensor [{rows}, {self.n}] in fp32 or bf16 (out's type) "
-                  f"on {dev} is needed")
-        with _On(dev):
-            st = _c.alspec_linear(
-                x.data_ptr(), 0 if rows <= 1 else x.stride(0), self.weight.data_ptr(),
-                0 if self.bias is None else self.bias.data_ptr(),
-                0 if residual is None else residual.data_ptr(), out.data_ptr(),
-                _c.ALSPEC_F32 if out.dtype is torch.float32 else _c.ALSPEC_BF16,
-                self.activation, rows, self.n, self.k, self.err.data_ptr(),
-                _stream(stream, dev))
+        if not (out.shape == (rows, n) and out.dtype in _FLOATS and out.device == dev
+                and out.is_contiguous()):
+            raise ValueError(f"out: a contiguous tensor [{rows}, {n}] in fp32 or bf16 on {dev} "
+                             f"is needed, got {out.dtype} {tuple(out.shape)} on {out.device}")
+        if residual is not None and not (residual.shape == (rows, n)
+                                         and residual.dtype is out.dtype
+                                         and residual.device == dev
+                                         and residual.is_contiguous()):
+            raise ValueError(f"residual: a contiguous tensor [{rows}, {n}] of out's type "
+                             f"{out.dtype} on {dev} is needed, got {residual.dtype} "
+                             f"{tuple(residual.shape)} on {residual.device}")
+        st = _on(self._index, _c._lib.alspec_linear, x.data_ptr(), 0 if rows <= 1 else xt[0],
+                 self.weight.data_ptr(), 0 if self.bias is None else self.bias.data_ptr(),
+                 0 if residual is None else residual.data_ptr(), out.data_ptr(),
+                 _CODES[out.dtype], self.activation, rows, n, self.k, self.err.data_ptr(),
+                 _stream(stream, self._index))
         if st:
             raise AlspecError(st, "alspec_linear")
         return out
 
     def device_error(self, stream=None):
         """(status, error word), read and cleared; synchronizes the stream."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        with _On(self.device), torch.cuda.stream(s):
-            word = int(self.err.item())
-            self.err.zero_()
-        return (_c.ALSPEC_ERR_TIMEOUT if word else _c.ALSPEC_OK), word
+        return _take_error(self.err, _c.ALSPEC_ERR_TIMEOUT, stream, self.device)

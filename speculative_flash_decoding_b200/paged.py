@@ -18,22 +18,13 @@ _CODES = {torch.float32: _c.ALSPEC_F32, torch.bfloat16: _c.ALSPEC_BF16,
           torch.float8_e4m3fn: _c.ALSPEC_E4M3}
 
 
-class _On:
-    """Makes `device` the current one around a call, where it is not."""
+_FLOATS = (torch.float32, torch.bfloat16)
 
-    __slots__ = ("index", "back")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
+# The raw handle of the current stream; torch.cuda.current_stream builds an
+# object around it, which took longer (2.2 us) than the checks and the launch
+# of a small call.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _device(device):
@@ -43,8 +34,16 @@ def _device(device):
     return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
 
 
-def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _stream(stream, index):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _on(index, fn, *args):
+    """fn(*args) with device `index` current."""
+    if _current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _want(ok, what):
@@ -52,22 +51,33 @@ def _want(ok, what):
         raise ValueError(what)
 
 
-def _index(t, name, shape, device):
-    """An int32 tensor that the kernels index with."""
-    _want(t.dtype is torch.int32 and t.device == device and tuple(t.shape) == shape
-          and t.is_contiguous(),
-          f"{name}: a contiguous int32 tensor of shape {shape} on {device} is needed, got "
-          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _index(t, name, n, device):
+    """Address of an int32 [n] tensor that the kernels index with."""
+    if not (t.dtype is torch.int32 and t.shape == (n,) and t.device == device
+            and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} on {device} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _table(page_table, device):
-    _want(page_table.dtype is torch.int32 and page_table.dim() == 2
-          and page_table.device == device and page_table.is_contiguous()
-          and page_table.shape[0] > 0 and page_table.shape[1] > 0,
-          "page_table: a contiguous int32 tensor [batch, max_pages] on the cache's device is "
-          "needed")
-    return page_table.data_ptr(), page_table.shape[0], page_table.shape[1]
+def _table(t, device):
+    """(batch, max_pages) of a page table."""
+    shape = t.shape
+    if not (t.dtype is torch.int32 and len(shape) == 2 and t.device == device
+            and t.is_contiguous() and shape[0] > 0 and shape[1] > 0):
+        raise ValueError("page_table: a contiguous int32 tensor [batch, max_pages] on the "
+                         f"cache's device {device} is needed, got {t.dtype} {tuple(shape)} on "
+                         f"{t.device}")
+    return shape
+
+
+def _take_error(err, code, stream, device):
+    """(status, word) of an error word, read and cleared; synchronizes."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        word = int(err.item())
+        err.zero_()
+    return (code if word else _c.ALSPEC_OK), word
 
 
 class PagedCache:
@@ -132,13 +142,13 @@ class PagedCache:
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = k, v, ks, vs
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n, h, s, d
         self.dtype, self.device = k.dtype, k.device
-        with _On(self.device):
-            self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         page, head, token = strides[0][:3]
         self.desc = _c.alspec_paged_cache(
             k.data_ptr(), v.data_ptr(), ks.data_ptr() if quantised else None,
             vs.data_ptr() if quantised else None, page, head, token, n, s, h, d,
             _CODES[k.dtype], 0)
+        self._index = self.device.index
         # Sizes and strides that no entry point takes are refused here.
         if _c.alspec_paged_workspace_size(self.desc, 1, h) == 0:
             raise AlspecError(_c.ALSPEC_ERR_UNSUPPORTED, "alspec_paged_workspace_size")
@@ -152,24 +162,23 @@ class PagedCache:
         device_error().  A token named twice gets a mixture of its values."""
         n = k.shape[0]
         row = (n, self.n_kv_heads, self.head_dim)
-        for name, t in (("k", k), ("v", v)):
-            _want(tuple(t.shape) == row and t.dtype is k.dtype and t.device == self.device
-                  and k.dtype in (torch.float32, torch.bfloat16)
-                  and t.stride(2) == 1
-                  and (self.n_kv_heads == 1 or t.stride(1) == self.head_dim),
-                  f"{name}: [n, n_kv_heads, head_dim] = {row} in fp32 or bf16 (both alike) on "
-                  f"{self.device}, heads side by side, is needed")
-        table, batch, max_pages = _table(page_table, self.device)
-        pos = _index(positions, "positions", (n,), self.device)
-        seq = 0 if seq_ids is None else _index(seq_ids, "seq_ids", (n,), self.device)
+        dev, one_head = self.device, self.n_kv_heads == 1
+        kt, vt = k.stride(), v.stride()
+        if not (k.shape == row and v.shape == row and k.dtype in _FLOATS and v.dtype is k.dtype
+                and k.device == dev and v.device == dev and kt[2] == 1 and vt[2] == 1
+                and (one_head or (kt[1] == self.head_dim and vt[1] == self.head_dim))):
+            raise ValueError("k and v: [n, n_kv_heads, head_dim] tensors in fp32 or bf16 (both "
+                             f"alike) on {dev}, heads side by side, are needed, got "
+                             f"{k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
+        batch, max_pages = _table(page_table, dev)
+        pos = _index(positions, "positions", n, dev)
+        seq = 0 if seq_ids is None else _index(seq_ids, "seq_ids", n, dev)
         if n == 0:
             return
-        one = n == 1
-        with _On(self.device):
-            st = _c.alspec_paged_append(
-                self.desc, k.data_ptr(), v.data_ptr(), _CODES[k.dtype],
-                0 if one else k.stride(0), 0 if one else v.stride(0), pos, seq, n, table, batch,
-                max_pages, self.err.data_ptr(), _stream(stream, self.device))
+        st = _on(self._index, _c._lib.alspec_paged_append, self.desc, k.data_ptr(), v.data_ptr(),
+                 _CODES[k.dtype], 0 if n == 1 else kt[0], 0 if n == 1 else vt[0], pos, seq, n,
+                 page_table.data_ptr(), batch, max_pages, self.err.data_ptr(),
+                 _stream(stream, self._index))
         if st:
             raise AlspecError(st, "alspec_paged_append")
 
@@ -177,21 +186,22 @@ class PagedCache:
         """Read pages back: rows [0, seq_lens[b]) of k_out and v_out [batch,
         n_kv_heads, max_seq_len, head_dim] (fp32 or bf16, contiguous) get the
         values of sequence b; the rows behind keep theirs.  Returns them."""
-        table, batch, max_pages = _table(page_table, self.device)
-        shape = (batch, self.n_kv_heads, k_out.shape[2] if k_out.dim() == 4 else 0,
-                 self.head_dim)
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            _want(tuple(t.shape) == shape and shape[2] > 0 and t.dtype is k_out.dtype
-                  and t.dtype in (torch.float32, torch.bfloat16) and t.device == self.device
-                  and t.is_contiguous(),
-                  f"{name}: a contiguous tensor [batch, n_kv_heads, max_seq_len, head_dim] in "
-                  f"fp32 or bf16 (both alike) on {self.device} is needed")
-        lens = _index(seq_lens, "seq_lens", (batch,), self.device)
-        with _On(self.device):
-            st = _c.alspec_paged_gather(
-                self.desc, table, max_pages, lens, batch, shape[2], _CODES[k_out.dtype],
-                k_out.data_ptr(), v_out.data_ptr(), self.err.data_ptr(),
-                _stream(stream, self.device))
+        dev = self.device
+        batch, max_pages = _table(page_table, dev)
+        shape = k_out.shape
+        if not (len(shape) == 4 and shape[0] == batch and shape[1] == self.n_kv_heads
+                and shape[2] > 0 and shape[3] == self.head_dim and v_out.shape == shape
+                and k_out.dtype in _FLOATS and v_out.dtype is k_out.dtype
+                and k_out.device == dev and v_out.device == dev
+                and k_out.is_contiguous() and v_out.is_contiguous()):
+            raise ValueError("k_out and v_out: contiguous tensors [batch, n_kv_heads, "
+                             f"max_seq_len, head_dim] in fp32 or bf16 (both alike) on {dev} are "
+                             f"needed, got {k_out.dtype} {tuple(shape)} and {v_out.dtype} "
+                             f"{tuple(v_out.shape)}")
+        lens = _index(seq_lens, "seq_lens", batch, dev)
+        st = _on(self._index, _c._lib.alspec_paged_gather, self.desc, page_table.data_ptr(),
+                 max_pages, lens, batch, shape[2], _CODES[k_out.dtype], k_out.data_ptr(),
+                 v_out.data_ptr(), self.err.data_ptr(), _stream(stream, self._index))
         if st:
             raise AlspecError(st, "alspec_paged_gather")
         return k_out, v_out
@@ -199,11 +209,7 @@ class PagedCache:
     def device_error(self, stream=None):
         """(status, error word) that append and gather left, read and
         cleared; synchronizes the stream."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        with _On(self.device), torch.cuda.stream(s):
-            word = int(self.err.item())
-            self.err.zero_()
-        return (_c.ALSPEC_ERR_DEVICE_DATA if word else _c.ALSPEC_OK), word
+        return _take_error(self.err, _c.ALSPEC_ERR_DEVICE_DATA, stream, self.device)
 
 
 class PagedDecoder:
@@ -215,13 +221,15 @@ class PagedDecoder:
         self.cache, self.batch, self.n_q_heads = cache, int(batch), int(n_q_heads)
         self.n_sink, self.window, self.scale = int(n_sink), int(window), float(scale)
         self.timeout_ms = int(timeout_ms)
-        with _On(cache.device):
-            nbytes = _c.alspec_paged_workspace_size(cache.desc, self.batch, self.n_q_heads)
-            if nbytes == 0:
-                raise AlspecError(_c.ALSPEC_ERR_INVALID_ARG, "alspec_paged_workspace_size")
-            self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
+        self._index = cache.device.index
+        nbytes = _on(self._index, _c.alspec_paged_workspace_size, cache.desc, self.batch,
+                     self.n_q_heads)
+        if nbytes == 0:
+            raise AlspecError(_c.ALSPEC_ERR_INVALID_ARG, "alspec_paged_workspace_size")
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
         self.workspace_bytes = nbytes
         self.q_dtype = torch.float32 if cache.dtype is torch.float32 else torch.bfloat16
+        self._shape = (self.batch, self.n_q_heads, cache.head_dim)
 
     def decode(self, q, page_table, seq_lens, out=None, lse=None, stream=None):
         """q [batch, n_q_heads, head_dim] (fp32 for fp32 pages, else bf16;
@@ -230,36 +238,35 @@ class PagedDecoder:
         sink set.  Fills out (fp32 or bf16; new: q's type) and, if given, lse
         (fp32 [batch, n_q_heads], natural logarithm); returns out."""
         c = self.cache
-        dev = c.device
-        shape = (self.batch, self.n_q_heads, c.head_dim)
-        _want(tuple(q.shape) == shape and q.dtype is self.q_dtype and q.device == dev
-              and q.stride(2) == 1 and (self.n_q_heads == 1 or q.stride(1) == c.head_dim),
-              f"q: {self.q_dtype} {shape} on {dev}, heads side by side, is needed")
+        dev, shape = c.device, self._shape
+        qt = q.stride()
+        if not (q.shape == shape and q.dtype is self.q_dtype and q.device == dev and qt[2] == 1
+                and (shape[1] == 1 or qt[1] == shape[2])):
+            raise ValueError(f"q: {self.q_dtype} {shape} on {dev}, heads side by side, is "
+                             f"needed, got {q.dtype} {tuple(q.shape)} on {q.device}")
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=dev)
-        _want(tuple(out.shape) == shape and out.dtype in (torch.float32, torch.bfloat16)
-              and out.device == dev and out.is_contiguous(),
-              f"out: a contiguous fp32 or bf16 tensor {shape} on {dev} is needed")
-        if lse is not None:
-            _want(tuple(lse.shape) == shape[:2] and lse.dtype is torch.float32
-                  and lse.device == dev and lse.is_contiguous(),
-                  f"lse: a contiguous fp32 tensor {shape[:2]} on {dev} is needed")
-        table, batch, max_pages = _table(page_table, dev)
-        _want(batch == self.batch, f"page_table: {self.batch} rows are needed, got {batch}")
-        lens = _index(seq_lens, "seq_lens", (self.batch,), dev)
-        with _On(dev):
-            st = _c.alspec_paged_decode(
-                c.desc, q.data_ptr(), 0 if self.batch == 1 else q.stride(0), self.n_q_heads,
-                table, max_pages, lens, self.batch, self.n_sink, self.window, self.scale,
-                _CODES[out.dtype], out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                self.timeout_ms, self.workspace.data_ptr(), self.workspace_bytes,
-                _stream(stream, dev))
+        elif not (out.shape == shape and out.dtype in _FLOATS and out.device == dev
+                  and out.is_contiguous()):
+            raise ValueError(f"out: a contiguous fp32 or bf16 tensor {shape} on {dev} is needed, "
+                             f"got {out.dtype} {tuple(out.shape)} on {out.device}")
+        if lse is not None and not (lse.shape == shape[:2] and lse.dtype is torch.float32
+                                    and lse.device == dev and lse.is_contiguous()):
+            raise ValueError(f"lse: a contiguous fp32 tensor {shape[:2]} on {dev} is needed")
+        batch, max_pages = _table(page_table, dev)
+        if batch != self.batch:
+            raise ValueError(f"page_table: {self.batch} rows are needed, got {batch}")
+        lens = _index(seq_lens, "seq_lens", batch, dev)
+        st = _on(self._index, _c._lib.alspec_paged_decode, c.desc, q.data_ptr(),
+                 0 if batch == 1 else qt[0], shape[1], page_table.data_ptr(), max_pages, lens,
+                 batch, self.n_sink, self.window, self.scale, _CODES[out.dtype], out.data_ptr(),
+                 0 if lse is None else lse.data_ptr(), self.timeout_ms,
+                 self.workspace.data_ptr(), self.workspace_bytes, _stream(stream, self._index))
         if st:
             raise AlspecError(st, "alspec_paged_decode")
         return out
 
     def device_error(self, stream=None):
         """(status, error word) of the workspace; see alspec_get_device_error."""
-        with _On(self.cache.device):
-            return _c.alspec_get_device_error(self.workspace.data_ptr(), self.workspace_bytes,
-                                              _stream(stream, self.cache.device))
+        return _on(self._index, _c.alspec_get_device_error, self.workspace.data_ptr(),
+                   self.workspace_bytes, _stream(stream, self._index))
