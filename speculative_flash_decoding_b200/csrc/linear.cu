@@ -150,6 +150,9 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     p.n = n;
     p.out_bf16 = out_dtype == ALSPEC_BF16;
     p.act = activation;
+    const uintptr_t quad = out_dtype == ALSPEC_F32 ? 15u : 7u;
+    p.vec = n % 4 == 0 && !(reinterpret_cast<uintptr_t>(y) & quad) &&
+            !(reinterpret_cast<uintptr_t>(residual) & quad);
     p.err = err;
     p.timeout_ns = 2000000000ull;
     const void* fn = reinterpret_cast<const void*>(linear_kernel);

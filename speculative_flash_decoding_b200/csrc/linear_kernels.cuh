@@ -30,7 +30,7 @@ constexpr int kLinMaxN = 256;     // batch rows per tile
 constexpr int kLinMaxStages = 12;
 constexpr int kLinRing = 200 * 1024;
 constexpr int kLinMaxSplit = 8;   // CTAs of a cluster
-constexpr int kLinAhead = 4;      // stages asked for before the kernel ahead has ended
+constexpr int kLinAhead = 8;      // blocks asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM
 // holds one CTA and its TMEM allocation never waits for another's.
 constexpr int kLinMinSmem = 120 * 1024;
@@ -49,6 +49,7 @@ struct LinearParams {
     int group;     // 64-column blocks a stage holds
     int tmem_cols;
     int out_bf16, act;
+    int vec;       // y and the residual can be taken four features at a time
     unsigned* err;
     unsigned long long timeout_ns;
 };
@@ -129,37 +130,95 @@ __device__ __forceinline__ float lin_value(const __nv_bfloat16* p) { return __bf
 __device__ __forceinline__ void lin_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void lin_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Bias, activation and residual of the sums of one feature in `count` <= N
-// batch rows from r on, and their way out.
-template <typename O, int N>
-__device__ __forceinline__ void lin_finish(const LinearParams& p, float (&v)[N], int r, int count,
-                                           int feature, float bias) {
-    const long long at = (long long)r * p.n + feature;
-    const O* res = p.residual ? static_cast<const O*>(p.residual) + at : nullptr;
-    O* y = static_cast<O*>(p.y) + at;
-    float add[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        add[i] = res && i < count ? lin_value(res + (long long)i * p.n) : 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += bias;
-    lin_activate(v, p.act);
-    if (res) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += add[i];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < count) lin_put(y + (long long)i * p.n, v[i]);
+// Four neighbouring values, aligned to their size.
+__device__ __forceinline__ float4 lin_value4(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+__device__ __forceinline__ float4 lin_value4(const __nv_bfloat16* p) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                       __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ void lin_put4(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void lin_put4(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
-template <int N>
-__device__ __forceinline__ void lin_out(const LinearParams& p, float (&v)[N], int r, int count,
-                                        int feature, float bias) {
-    if (p.out_bf16)
-        lin_finish<__nv_bfloat16>(p, v, r, count, feature, bias);
-    else
-        lin_finish<float>(p, v, r, count, feature, bias);
+// The epilogue of batch rows [c0, c1) of a tile whose sums lie in shared
+// memory, [row][feature], one part in each of the cluster's CTAs.  A warp
+// takes a row at a time, a lane four features; everything a round of
+// kLinRows rows needs is asked for before it is used.
+constexpr int kLinRows = 4;
+
+template <typename O>
+__device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int c0, int c1,
+                                             int r0, int n0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = kLinThreads / 32;
+    const int f = n0 + 4 * lane;
+    const int nf = min(4, p.n - f);  // features of this lane
+    if (nf <= 0) return;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < nf) bias[i] = __bfloat162float(p.bias[f + i]);
+    }
+    for (int c = c0 + warp; c < c1; c += kWarps * kLinRows) {
+        const long long at = (long long)(r0 + c) * p.n + f;
+        const long long step = (long long)kWarps * p.n;
+        const O* res = static_cast<const O*>(p.residual);
+        float v[4 * kLinRows], add[4 * kLinRows];
+        if (res) {
+#pragma unroll
+            for (int u = 0; u < kLinRows; ++u) {
+                if (c + u * kWarps >= c1) continue;
+                if (p.vec) {
+                    const float4 x = lin_value4(res + at + u * step);
+                    add[4 * u] = x.x, add[4 * u + 1] = x.y, add[4 * u + 2] = x.z, add[4 * u + 3] = x.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < nf) add[4 * u + i] = lin_value(res + at + u * step + i);
+                }
+            }
+        }
+        for (int s = 0; s < p.split; ++s) {
+            const uint32_t from = dsmem_addr(sums + (uint32_t)(c * kLinM + 4 * lane) * 4, s);
+            float4 part[kLinRows];
+#pragma unroll
+            for (int u = 0; u < kLinRows; ++u)
+                if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
+#pragma unroll
+            for (int u = 0; u < kLinRows; ++u) {
+                v[4 * u] = s ? v[4 * u] + part[u].x : part[u].x;
+                v[4 * u + 1] = s ? v[4 * u + 1] + part[u].y : part[u].y;
+                v[4 * u + 2] = s ? v[4 * u + 2] + part[u].z : part[u].z;
+                v[4 * u + 3] = s ? v[4 * u + 3] + part[u].w : part[u].w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * kLinRows; ++i) v[i] += bias[i % 4];
+        lin_activate(v, p.act);
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < 4 * kLinRows; ++i) v[i] += add[i];
+        }
+        O* y = static_cast<O*>(p.y);
+#pragma unroll
+        for (int u = 0; u < kLinRows; ++u) {
+            if (c + u * kWarps >= c1) continue;
+            if (p.vec) {
+                lin_put4(y + at + u * step, v + 4 * u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < nf) lin_put(y + at + u * step + i, v[4 * u + i]);
+            }
+        }
+    }
 }
 
 __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
@@ -180,6 +239,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     const int kb1 = (int)((long long)(rank + 1) * p.kblocks / p.split);
     const int stage_bytes = (kLinM + p.nt) * 128 * p.group;
     const int fills = (kb1 - kb0 + p.group - 1) / p.group;
+    const int rows = min(p.nt, p.rows - r0);
+    const int c0 = rank * rows / p.split, c1 = (rank + 1) * rows / p.split;  // this CTA finishes
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -211,7 +272,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     // (W's first stages are asked for in L2 meanwhile, which is coherent
     // whoever writes them: 16 x 8192 x 8192 back to back 25.9 -> 24.5 us.)
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < min(kLinAhead, fills); ++i) {
+        for (int i = 0; i < kLinAhead / p.group; ++i) {
             const int kb = kb0 + i * p.group;
             if (kb + p.group <= min(kb1, p.whole)) tma_prefetch_3d(&p.tw, 0, n0, kb);
         }
@@ -274,6 +335,15 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
             }
             lin_commit(&done);
         }
+    } else if (p.residual) {
+        // Meanwhile the residual is asked for in L2.
+        const int es = p.out_bf16 ? 2 : 4;
+        const int lines = (kLinM * es + 127) / 128;
+        const char* res = static_cast<const char*>(p.residual);
+        for (int i = threadIdx.x - 64; i < (c1 - c0) * lines; i += kLinThreads - 64) {
+            const int f = n0 + i % lines * (128 / es);
+            if (f < p.n) prefetch_l2(res + ((long long)(r0 + c0 + i / lines) * p.n + f) * es);
+        }
     }
     __syncwarp();
     // The accumulator is complete (each thread waits; bounded).
@@ -281,52 +351,30 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     __syncthreads();
 
-    // Warp w reads the 32 lanes of its quarter; the two halves of the warps
-    // take alternate groups of 16 columns.
-    const int quarter = warp & 3, half = warp >> 2;
-    const int fl = quarter * 32 + lane;  // feature within the tile
-    const int feature = n0 + fl;
-    const bool live = feature < p.n && good;
-    const float bias = live && p.bias ? __bfloat162float(p.bias[feature]) : 0.f;
-    const int rows = min(p.nt, p.rows - r0);
-    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
-    if (p.split == 1) {
-        for (int c = 16 * half; c < rows; c += 32) {
-            float v[16];
-            lin_load16(taddr + c, v);
-            if (live) lin_out(p, v, r0 + c, min(16, rows - c), feature, bias);
-            __syncwarp();
-        }
-    } else {
-        // This CTA's part of the sums, [batch row][feature], where the ring
-        // was; then every CTA of the cluster adds its share of the rows.
-        float* mine = reinterpret_cast<float*>(ring);
-        for (int c = 16 * half; c < rows; c += 32) {
-            float v[16];
-            lin_load16(taddr + c, v);
+    // This CTA's sums, [batch row][feature], go where the ring was (warp w
+    // reads the 32 lanes of its quarter, the two halves of the warps take
+    // alternate groups of 16 columns); then every CTA of the cluster finishes
+    // its share of the rows.
+    float* mine = reinterpret_cast<float*>(ring);
+    const int fl = (warp & 3) * 32 + lane;  // feature within the tile
+    const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    for (int c = 16 * (warp >> 2); c < rows; c += 32) {
+        float v[16];
+        lin_load16(taddr + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + fl] = v[i];
-        }
-        cluster_sync();
-        const int c1 = (rank + 1) * rows / p.split;
-        const uint32_t base = smem_addr(mine) + fl * 4;
-        if (live) {
-            for (int c = rank * rows / p.split + 8 * half; c < c1; c += 16) {
-                float v[8];
-                for (int s = 0; s < p.split; ++s) {
-                    const uint32_t at = dsmem_addr(base + c * kLinM * 4, s);
-                    float part[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        part[i] = c + i < c1 ? ld_dsmem(at + i * kLinM * 4) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = s == 0 ? part[i] : v[i] + part[i];
-                }
-                lin_out(p, v, r0 + c, min(8, c1 - c), feature, bias);
-            }
-        }
-        cluster_sync();
+        for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + fl] = v[i];
     }
+    if (p.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (good) {
+        if (p.out_bf16)
+            lin_epilogue<__nv_bfloat16>(p, smem_addr(mine), c0, c1, r0, n0);
+        else
+            lin_epilogue<float>(p, smem_addr(mine), c0, c1, r0, n0);
+    }
+    if (p.split > 1) cluster_sync();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (warp == 2)

@@ -120,18 +120,38 @@ struct PagedKernel {
     int threads, smem, part_floats;
 };
 
-template <int T, int D>
+template <int T, int D, int BOX>
 PagedKernel paged_kernel() {
-    using C = PagedCfg<T, D>;
-    return PagedKernel{paged_decode_kernel<T, D>, C::kThreads, C::kSmemBytes, C::PART};
+    using C = PagedCfg<T, D, BOX>;
+    return PagedKernel{paged_decode_kernel<T, D, BOX>, C::kThreads, C::kSmemBytes, C::PART};
+}
+
+// Rows of up to 128 bytes lie the same way whatever the box.
+template <int T, int D>
+PagedKernel paged_kernel_box(int box) {
+    if constexpr (PagedCfg<T, D, kTile>::SEGS > 1) {
+        if (box == 8) return paged_kernel<T, D, 8>();
+        if (box == 16) return paged_kernel<T, D, 16>();
+    }
+    return paged_kernel<T, D, kTile>();
 }
 
 template <int D>
-PagedKernel paged_kernel_for(int dtype, int out_dtype) {
-    return dtype == ALSPEC_F32        ? paged_kernel<kPagesF32, D>()
-           : dtype == ALSPEC_E4M3     ? paged_kernel<kPagesE4m3, D>()
-           : out_dtype == ALSPEC_BF16 ? paged_kernel<kPagesBf16, D>()
-                                      : paged_kernel<kPagesBf16Wide, D>();
+PagedKernel paged_kernel_type(int dtype, int out_dtype, int box) {
+    return dtype == ALSPEC_F32        ? paged_kernel_box<kPagesF32, D>(box)
+           : dtype == ALSPEC_E4M3     ? paged_kernel_box<kPagesE4m3, D>(box)
+           : out_dtype == ALSPEC_BF16 ? paged_kernel_box<kPagesBf16, D>(box)
+                                      : paged_kernel_box<kPagesBf16Wide, D>(box);
+}
+
+// Rows of a TMA box: the largest power of two up to a tile that divides a
+// page (8, 16 or 32).
+int box_rows(int page_size) { return std::min(kTile, page_size & -page_size); }
+
+PagedKernel paged_kernel_for(const alspec_paged_cache& c, int out_dtype) {
+    const int box = box_rows(c.page_size);
+    return c.head_dim == 128 ? paged_kernel_type<128>(c.dtype, out_dtype, box)
+                             : paged_kernel_type<64>(c.dtype, out_dtype, box);
 }
 
 // Workspace: the error word and one ticket per CTA, two partials per CTA for
@@ -158,28 +178,30 @@ alspec_status check_heads(const alspec_paged_cache* c, int batch, int n_q_heads)
     return ALSPEC_OK;
 }
 
-// A 4-D view (head_dim, slot, KV head, page) of a pool; boxes of one column
-// segment (128 bytes, or a whole row of 64) and `box` slots.
+// A 5-D view (element, slot, 128-byte segment, KV head, page) of a pool (rows
+// of 64 bytes: one segment); boxes of `box` slots with all their segments.
 alspec_status encode_pages(CUtensorMap* map, const void* base, const alspec_paged_cache& c,
                            const PageLayout& l, int box) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     const alspec_status st = tiled_map_encoder(&encode);
     if (st != ALSPEC_OK) return st;
     const int es = elem_size(c.dtype);
-    const int row = c.head_dim * es;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
-                                (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)(l.token_stride * es),
+    const int row = c.head_dim * es, seg = std::min(row, 128);
+    const cuuint64_t dims[5] = {(cuuint64_t)(seg / es), (cuuint64_t)c.page_size,
+                                (cuuint64_t)(row / seg), (cuuint64_t)c.n_kv_heads,
+                                (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)(l.token_stride * es), (cuuint64_t)seg,
                                    (cuuint64_t)(l.head_stride * es),
                                    (cuuint64_t)(l.page_stride * es)};
-    const cuuint32_t boxes[4] = {(cuuint32_t)(std::min(row, 128) / es), (cuuint32_t)box, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const cuuint32_t boxes[5] = {(cuuint32_t)(seg / es), (cuuint32_t)box,
+                                 (cuuint32_t)(row / seg), 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUresult r = encode(
         map,
         c.dtype == ALSPEC_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
         : c.dtype == ALSPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                  : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-        4, const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        5, const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
         row >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ALSPEC_OK : ALSPEC_ERR_INVALID_ARG;
@@ -275,8 +297,7 @@ alspec_status alspec_paged_gather(const alspec_paged_cache* cache, const int32_t
 
 size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, int n_q_heads) {
     if (check_heads(cache, batch, n_q_heads) != ALSPEC_OK) return 0;
-    const PagedKernel k = cache->head_dim == 128 ? paged_kernel_for<128>(cache->dtype, ALSPEC_F32)
-                                                 : paged_kernel_for<64>(cache->dtype, ALSPEC_F32);
+    const PagedKernel k = paged_kernel_for(*cache, ALSPEC_F32);
     return workspace_bytes_for(k, sm_count_for_plan());
 }
 
@@ -300,9 +321,7 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
                           q_stride >= ((int64_t)1 << 40)))
         return ALSPEC_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return ALSPEC_ERR_WORKSPACE;
-    const PagedKernel kern = cache->head_dim == 128
-                                 ? paged_kernel_for<128>(cache->dtype, out_dtype)
-                                 : paged_kernel_for<64>(cache->dtype, out_dtype);
+    const PagedKernel kern = paged_kernel_for(*cache, out_dtype);
     const int ctas = sm_count_for_plan();
     if (workspace_bytes < workspace_bytes_for(kern, ctas)) return ALSPEC_ERR_WORKSPACE;
     if ((st = smem_attr_once(reinterpret_cast<const void*>(kern.fn), kern.smem)) != ALSPEC_OK)
@@ -310,8 +329,7 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
 
     PagedParams p{};
     const PageLayout l = layout_of(*cache);
-    // Rows of a box: the largest power of two up to a tile that divides a page.
-    p.box = std::min(kTile, cache->page_size & -cache->page_size);
+    p.box = box_rows(cache->page_size);
     if ((st = encode_pages(&p.tk, cache->k_pages, *cache, l, p.box)) != ALSPEC_OK) return st;
     if ((st = encode_pages(&p.tv, cache->v_pages, *cache, l, p.box)) != ALSPEC_OK) return st;
     p.q = q;

@@ -252,7 +252,7 @@ constexpr int kHeadRows = 8;    // query heads per work unit
 enum : int { kPagesF32 = 0, kPagesBf16 = 1, kPagesE4m3 = 2, kPagesBf16Wide = 3 };
 
 struct PagedParams {
-    CUtensorMap tk, tv;  // 4-D: (head_dim, slot, KV head, page)
+    CUtensorMap tk, tv;  // 5-D: (element, slot, 128-byte segment, KV head, page)
     const void* q;
     long long q_stride;
     const float* ks;
@@ -277,19 +277,34 @@ struct PagedParams {
 
 constexpr int kPagedTickets = kCtrFixed;  // one ticket per CTA follows
 
-template <int T, int D>
+// BOX: rows of a TMA box, as far as the layout in shared memory depends on it
+// (rows of more than 128 bytes: a box holds its rows segment by segment).
+template <int T, int D, int BOX>
 struct PagedCfg {
     static constexpr int ES = T == kPagesF32 ? 4 : T == kPagesE4m3 ? 1 : 2;
     static constexpr int RB = D * ES;                     // bytes of a row
     static constexpr int SEGB = RB < 128 ? RB : 128;      // bytes of a box row
     static constexpr int SEGS = RB / SEGB;                // boxes side by side
-    static constexpr int SEG_TILE = kTile * SEGB;         // one segment of a tile
+    static constexpr int SEG = BOX * SEGB;                // one segment of a box
     static constexpr int TILEB = kTile * RB;              // K or V of a tile
     static constexpr int STAGEB = 2 * TILEB;
     // Warps, and stages per warp, of a 192 KB ring.
-    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? 6 : STAGEB >= 8192 ? 8 : 16;
+#ifndef NW16
+#define NW16 6
+#endif
+#ifndef NW8
+#define NW8 8
+#endif
+#ifndef NW4
+#define NW4 16
+#endif
+    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? NW16 : STAGEB >= 8192 ? NW8 : NW4;
     static constexpr int ST = 196608 / STAGEB / NW;
     static constexpr int kThreads = NW * 32;
+    // Offset of a row (a multiple of 8, or its row within 8 added later).
+    __host__ __device__ static constexpr int row(int r) {
+        return r / BOX * (SEGS * SEG) + r % BOX * SEGB;
+    }
     static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
     static constexpr int kOffScale = NW * ST * STAGEB;
     static constexpr int kOffMeta = kOffScale + (T == kPagesE4m3 ? NW * ST * 2 * kTile * 4 : 0);
@@ -385,7 +400,8 @@ __device__ __forceinline__ long long share_of(long long total, long long workers
 // A run of tiles of one (sequence, unit) that did not end where it began.
 struct PagedPiece {
     int b, u, lo, hi;  // tiles [lo, hi) of n; hi == 0: none
-    int n, pad[3];
+    int n, c0, c1;     // the CTAs that share the (sequence, unit)
+    int pad;
 };
 
 // Two neighbouring elements of the output.
@@ -410,9 +426,34 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-template <int T, int D>
+// Partials of one head joined: running maximum, sum, four weighted values.
+struct PagedSum {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    __device__ __forceinline__ void add(float pm, float pl, const float4& v) {
+        const float M = fmaxf(m, pm);
+        const float f = merge_weight(m, M), g = merge_weight(pm, M);
+        m = M;
+        l = l * f + pl * g;
+        o.x = o.x * f + v.x * g;
+        o.y = o.y * f + v.y * g;
+        o.z = o.z * f + v.z * g;
+        o.w = o.w * f + v.w * g;
+    }
+    // Elements e .. e + 3 of the rows of D elements from head `head0` on.
+    template <int D>
+    __device__ __forceinline__ void write(const PagedParams& p, long long head0, int e) const {
+        const float inv = paged_inverse(l);
+        paged_store2(p, head0 * D + e, o.x * inv, o.y * inv);
+        paged_store2(p, head0 * D + e + 2, o.z * inv, o.w * inv);
+        if (p.lse && e % D == 0) p.lse[head0 + e / D] = paged_lse(m, l);
+    }
+};
+
+template <int T, int D, int BOX>
 struct PagedWarp {
-    using C = PagedCfg<T, D>;
+    using C = PagedCfg<T, D, BOX>;
     static constexpr bool kB16 = T == kPagesBf16 || T == kPagesBf16Wide;
     static constexpr int KS = T == kPagesF32 ? D / 8 : D / 16;  // k steps of Q K
     static constexpr int NT = D / 8;                            // output n tiles
@@ -434,7 +475,7 @@ struct PagedWarp {
         if constexpr (T == kPagesF32)
             v_off = (uint32_t)(2 * j * 128 + (((lane >> 4) ^ (2 * j)) << 4) + ((lane >> 2) & 3) * 4);
         else
-            v_off = (uint32_t)((mat & 1) * 8 * C::SEGB + row8 * C::SEGB + (((mat >> 1) ^ sw) << 4));
+            v_off = (uint32_t)((mat & 1) * C::row(8) + row8 * C::SEGB + (((mat >> 1) ^ sw) << 4));
     }
 
     __device__ __forceinline__ void reset() {
@@ -546,8 +587,8 @@ struct PagedWarp {
 #pragma unroll
             for (int c = 0; c < CH; c += 4) {
                 uint32_t f[4];
-                ldsm_x4(ka[(c >> 2) & 1] + (uint32_t)(n * 8 * C::SEGB + (c >> 3) * C::SEG_TILE),
-                        f[0], f[1], f[2], f[3]);
+                ldsm_x4(ka[(c >> 2) & 1] + (uint32_t)(C::row(8 * n) + (c >> 3) * C::SEG), f[0],
+                        f[1], f[2], f[3]);
                 if constexpr (kB16) {
                     mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[0], f[1]);
                     mma_bf16_16816(s[n], qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, f[2], f[3]);
@@ -576,7 +617,8 @@ struct PagedWarp {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) x[n][i] = kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i];
+            for (int i = 0; i < 2; ++i)
+                x[n][i] = kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i];
             if constexpr (T == kPagesE4m3) {
                 const float2 kk = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * j);
                 const float2 vv = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * j);
@@ -647,7 +689,7 @@ struct PagedWarp {
                 split_tf32(x[n][1], h1, l1);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const uint32_t add = (uint32_t)(n * 1024 + (i >> 2) * C::SEG_TILE);
+                    const uint32_t add = (uint32_t)(C::row(8 * n) + (i >> 2) * C::SEG);
                     const uint32_t flip = (uint32_t)((2 * i & 7) << 4);
                     uint32_t a0, a1, b0, b1;
                     split_tf32(lds((v0 ^ flip) + add), a0, a1);
@@ -679,7 +721,7 @@ struct PagedWarp {
                 for (int c = 0; c < CH; c += 2) {
                     uint32_t f4[4];
                     ldsm_x4_t((v0 ^ (uint32_t)((c & 7) << 4)) +
-                                  (uint32_t)(k * 16 * C::SEGB + (c >> 3) * C::SEG_TILE),
+                                  (uint32_t)(C::row(16 * k) + (c >> 3) * C::SEG),
                               f4[0], f4[1], f4[2], f4[3]);
                     if constexpr (T == kPagesE4m3) {
                         // A code pair of one token per half word: split into
@@ -763,10 +805,10 @@ struct PagedWarp {
     }
 };
 
-template <int T, int D>
-__global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kernel(
+template <int T, int D, int BOX>
+__global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode_kernel(
     const __grid_constant__ PagedParams p) {
-    using C = PagedCfg<T, D>;
+    using C = PagedCfg<T, D, BOX>;
     extern __shared__ unsigned char pd_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(pd_raw) + 1023) & ~uintptr_t(1023));
@@ -818,48 +860,47 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
         PagedPos pos = paged_find(p, x0);
         const PagedPos start = pos;
         const uint64_t pol = p.blocks == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
-        // A box is `box` rows of one 128-byte column segment of K or V; the
-        // boxes of a tile are spread over the lanes: lane = sub-box +
-        // boxes-down * (segment, K or V).
-        const int down = kTile / p.box;
-        const int sub = lane & (down - 1), first = lane / down, step = kTile / down;
-        const int from = lane / p.box, rem = lane % p.box;
-        int page = 0;    // of this lane's sub-box in the next tile to be issued
+        // A tile comes in boxes of `box` rows, K's and V's; lane i keeps the
+        // page of box i.
+        const int box = C::SEGS > 1 ? BOX : p.box;
+        const int down = kTile / box;
+        const int sub = lane & (down - 1);
+        const int from = lane / box, rem = lane % box;
+        int page = 0;    // of this lane's box in the next tile to be issued
         int in_page = 0;
         int t0 = 0;      // that tile's first token
         auto fetch_page = [&]() {
             t0 = (pos.i < pos.s.a ? pos.i : pos.i + pos.s.f - pos.s.a) * kTile;
-            const int t = t0 + sub * p.box;
+            const int t = t0 + sub * box;
             const int entry = (int)(__umulhi((unsigned)t, p.page_mul) >> p.page_shift);
             in_page = t - entry * p.page_size;
             if (t < pos.s.len) page = __ldg(p.table + (long long)pos.b * p.max_pages + entry);
         };
         auto issue = [&](int slot) {
             const int left = pos.s.len - t0;  // tokens from here on
-            const bool mine = sub * p.box < left;
             const int h = p.blocks == 1 ? pos.u : pos.u / p.blocks;
             unsigned char* stage = ring + slot * C::STAGEB;
-            if (lane == 0) {
-                const int boxes = left >= kTile ? down : (left + p.box - 1) / p.box;
-                meta[slot] = make_int4(pos.b, pos.u, pos.i, t0);
-                mbar_arrive_expect_tx(full + slot, (uint32_t)(boxes * p.box * 2 * C::RB));
+            const int boxes = left >= kTile ? down : (left + box - 1) / box;
+            if (sub < boxes && (unsigned)page >= (unsigned)p.n_pages) {
+                atomicOr(p.ctr + kCtrError, kErrPage);
+                page = 0;
             }
             __syncwarp();
-            if (mine) {
-                if ((unsigned)page >= (unsigned)p.n_pages) {
-                    atomicOr(p.ctr + kCtrError, kErrPage);
-                    page = 0;
-                }
-                for (int c = first; c < 2 * C::SEGS; c += step) {
-                    const int v = c & 1, seg = c >> 1;
-                    tma_load_4d(stage + v * C::TILEB + seg * C::SEG_TILE + sub * p.box * C::SEGB,
-                                v ? &p.tv : &p.tk, seg * (C::SEGB / C::ES), in_page, h, page,
-                                full + slot, pol);
+            if (elect_one()) {
+                meta[slot] = make_int4(pos.b, pos.u, pos.i, t0);
+                mbar_arrive_expect_tx(full + slot, (uint32_t)(boxes * box * 2 * C::RB));
+            }
+            for (int i = 0; i < boxes; ++i) {
+                const int pg = __shfl_sync(0xffffffffu, page, i);
+                const int in = __shfl_sync(0xffffffffu, in_page, i);
+                unsigned char* dst = stage + i * (box * C::RB);
+                if (elect_one()) {
+                    tma_load_5d(dst, &p.tk, in, h, pg, full + slot, pol);
+                    tma_load_5d(dst + C::TILEB, &p.tv, in, h, pg, full + slot, pol);
                 }
             }
             if constexpr (T == kPagesE4m3) {
                 // Lane = token: its scales, and its arrival once they landed.
-                __syncwarp();
                 const int pg = __shfl_sync(0xffffffffu, page, from);
                 const int in = __shfl_sync(0xffffffffu, in_page, from) + rem;
                 if (lane < left) {
@@ -886,25 +927,26 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
         fetch_page();
         int issued = 0;
         for (; issued < min(C::ST, tiles); ++issued) issue(issued);
+        __syncwarp();
 
-        PagedWarp<T, D> state;
+        PagedWarp<T, D, BOX> state;
         state.init(lane);
         state.reset();
         state.load_q(p, start.b, start.u, lane);
         PagedSeq s = start.s;
         {
-            // What this warp leaves to be joined.
+            // What this warp leaves to be joined, and with which CTAs.
             const PagedPos end = paged_find(p, x0 + tiles - 1);
-            tail.b = end.b, tail.u = end.u, tail.n = end.s.n;
-            if (end.b == start.b && end.u == start.u) {
-                if (start.i > 0 || end.i + 1 < end.s.n) tail.lo = start.i, tail.hi = end.i + 1;
-            } else {
-                if (start.i > 0) {
-                    head.b = start.b, head.u = start.u, head.lo = start.i;
-                    head.hi = head.n = start.s.n;
-                }
-                if (end.i + 1 < end.s.n) tail.hi = end.i + 1;
-            }
+            auto piece = [&](PagedPiece& q, const PagedPos& at, long long tile0, int lo, int hi) {
+                q.b = at.b, q.u = at.u, q.n = at.s.n, q.lo = lo, q.hi = hi;
+                q.c0 = (int)(share_of(total, workers, tile0) / C::NW);
+                q.c1 = (int)(share_of(total, workers, tile0 + q.n - 1) / C::NW);
+            };
+            const bool one = end.b == start.b && end.u == start.u;
+            const int lo = one ? start.i : 0;
+            if (!one && start.i > 0) piece(head, start, x0 - start.i, start.i, start.s.n);
+            if (lo > 0 || end.i + 1 < end.s.n)
+                piece(tail, end, x0 + tiles - 1 - end.i, lo, end.i + 1);
         }
         empty_rows();
         int done = 0, slot = 0;
@@ -941,8 +983,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
                 if (!on) {
                     for (int g = 0; g < C::SEGS; ++g)
                         for (int c = 0; c < C::SEGB; c += 16)
-                            *reinterpret_cast<uint4*>(stage + C::TILEB + g * C::SEG_TILE +
-                                                      lane * C::SEGB + c) =
+                            *reinterpret_cast<uint4*>(stage + C::TILEB + C::row(lane) +
+                                                      g * C::SEG + c) =
                                 make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
@@ -997,109 +1039,107 @@ __global__ void __launch_bounds__(PagedCfg<T, D>::kThreads, 1) paged_decode_kern
     __syncthreads();
 
     // Join what spans warps: runs of pieces of one (sequence, unit).  Piece 2 i
-    // is warp i's first run, piece 2 i + 1 its last.
+    // is warp i's first run, piece 2 i + 1 its last; every lane holds one.
     auto partial = [&](int i) {
         return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * C::ST * C::STAGEB)
                        : p.heads + ((long long)blockIdx.x * C::NW + (i >> 1)) * C::PART;
     };
-    for (int i = 0; i < 2 * C::NW;) {
-        const PagedPiece a = pieces[i];
-        if (a.hi == 0) {
-            ++i;
-            continue;
-        }
-        int k = i, hi = 0;
-        unsigned there = 0;
-        for (; k < 2 * C::NW; ++k) {
-            if (pieces[k].hi == 0) continue;
-            if (pieces[k].b != a.b || pieces[k].u != a.u) break;
-            hi = pieces[k].hi;
-            there |= 1u << k;
-        }
-        const bool whole = a.lo == 0 && hi == a.n;
-        const int rows = min(kHeadRows, p.group - (a.u % p.blocks) * kHeadRows);
-        const long long head0 = (long long)a.b * p.hq + (a.u / p.blocks) * p.group +
-                                (a.u % p.blocks) * kHeadRows;
-        // A run that began in an earlier CTA is this CTA's first partial, one
-        // that goes on in the next its second.
-        float* mine = p.part + ((long long)blockIdx.x * 2 + (a.lo == 0 ? 1 : 0)) * C::PART;
-        for (int e = 4 * threadIdx.x; e < rows * D; e += 4 * C::kThreads) {
+    static_assert(2 * C::NW <= 32, "a lane per piece");
+    PagedPiece a{};
+    if (lane < 2 * C::NW) a = pieces[lane];
+    const unsigned there = __ballot_sync(0xffffffffu, a.hi > 0);
+    const unsigned before = there & ((1u << lane) - 1u);
+    const int prev = before ? 31 - __clz(before) : lane;
+    const int pb = __shfl_sync(0xffffffffu, a.b, prev), pu = __shfl_sync(0xffffffffu, a.u, prev);
+    const unsigned starts = __ballot_sync(
+        0xffffffffu, a.hi > 0 && (before == 0 || pb != a.b || pu != a.u));
+    auto rows_of = [&](int u) { return min(kHeadRows, p.group - (u % p.blocks) * kHeadRows); };
+    auto head_of = [&](int b, int u) {
+        return (long long)b * p.hq + (u / p.blocks) * p.group + (u % p.blocks) * kHeadRows;
+    };
+    // A run that began in an earlier CTA is this CTA's first partial, one that
+    // goes on in the next its second.  Runs go round the warps.
+    int open[2] = {-1, -1};  // the pieces that begin them
+    int turn = 0;
+    for (unsigned left = starts; left; left &= left - 1, ++turn) {
+        const int i = __ffs(left) - 1;
+        const unsigned next = left & (left - 1);
+        const unsigned run = there & ~((1u << i) - 1u) & (next ? (next & -next) - 1u : ~0u);
+        const int lo = __shfl_sync(0xffffffffu, a.lo, i);
+        const int hi = __shfl_sync(0xffffffffu, a.hi, 31 - __clz(run));
+        const bool whole = lo == 0 && hi == __shfl_sync(0xffffffffu, a.n, i);
+        const int part = lo == 0 ? 1 : 0;
+        if (!whole) open[part] = i;
+        if (turn % C::NW != warp) continue;
+        const int b = __shfl_sync(0xffffffffu, a.b, i), u = __shfl_sync(0xffffffffu, a.u, i);
+        const long long head0 = head_of(b, u);
+        float* mine = p.part + ((long long)blockIdx.x * 2 + part) * C::PART;
+        for (int e = 4 * lane; e < rows_of(u) * D; e += 128) {
             const int r = e / D;
-            float M = -INFINITY;
-            for (unsigned left = there; left; left &= left - 1)
-                M = fmaxf(M, partial(__ffs(left) - 1)[r]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-            for (unsigned left = there; left; left &= left - 1) {
-                const float* q = partial(__ffs(left) - 1);
-                const float f = merge_weight(q[r], M);
-                const float4 v = *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e);
-                o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
-                l += q[kHeadRows + r] * f;
+            PagedSum sum;
+            for (unsigned k = run; k; k &= k - 1) {
+                const float* q = partial(__ffs(k) - 1);
+                sum.add(q[r], q[kHeadRows + r],
+                        *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e));
             }
             if (whole) {
-                const float inv = paged_inverse(l);
-                paged_store2(p, head0 * D + e, o.x * inv, o.y * inv);
-                paged_store2(p, head0 * D + e + 2, o.z * inv, o.w * inv);
-                if (p.lse && e % D == 0) p.lse[head0 + r] = paged_lse(M, l);
+                sum.write<D>(p, head0, e);
             } else {
-                __stcg(reinterpret_cast<float4*>(mine + 2 * kHeadRows + e), o);
+                __stcg(reinterpret_cast<float4*>(mine + 2 * kHeadRows + e), sum.o);
                 if (e % D == 0) {
-                    __stcg(mine + r, M);
-                    __stcg(mine + kHeadRows + r, l);
+                    __stcg(mine + r, sum.m);
+                    __stcg(mine + kHeadRows + r, sum.l);
                 }
             }
         }
-        if (!whole) {
-            // The last CTA of this (sequence, unit) to arrive joins it.
-            if (threadIdx.x == 0) {
-                // Tile 0 of the run in the numbering, from one of its tiles.
-                const long long wi = (long long)blockIdx.x * C::NW + (i >> 1);
-                const long long begin = (i & 1) && a.lo == 0
-                                            ? share_begin(total, workers, wi + 1) - a.hi
-                                            : share_begin(total, workers, wi) - a.lo;
-                misc[2] = (int)(share_of(total, workers, begin) / C::NW);
-                misc[3] = (int)(share_of(total, workers, begin + a.n - 1) / C::NW);
-            }
-            __syncthreads();
-            const int c0 = misc[2], c1 = misc[3];
-            if (threadIdx.x == 0) {
-                // Releases what the CTA wrote before the barrier, and takes
-                // what the others released.
-                const unsigned old = atom_add_acq_rel_gpu(p.ctr + kPagedTickets + c0, 1u);
-                misc[1] = old == (unsigned)(c1 - c0) ? 1 : 0;
-                if (old == (unsigned)(c1 - c0)) p.ctr[kPagedTickets + c0] = 0u;
-            }
-            __syncthreads();
-            if (misc[1]) {
-                for (int e = 4 * threadIdx.x; e < rows * D; e += 4 * C::kThreads) {
-                    const int r = e / D;
-                    auto slot = [&](int c) {
-                        return p.part + ((long long)c * 2 + (c == c0)) * C::PART;
-                    };
-                    float M = -INFINITY;
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot(c) + r));
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float l = 0.f;
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* q = slot(c);
-                        const float f = merge_weight(__ldcg(q + r), M);
-                        const float4 v = __ldcg(
-                            reinterpret_cast<const float4*>(q + 2 * kHeadRows + e));
-                        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
-                        l += __ldcg(q + kHeadRows + r) * f;
-                    }
-                    const float inv = paged_inverse(l);
-                    paged_store2(p, head0 * D + e, o.x * inv, o.y * inv);
-                    paged_store2(p, head0 * D + e + 2, o.z * inv, o.w * inv);
-                    if (p.lse && e % D == 0) p.lse[head0 + r] = paged_lse(M, l);
+        __syncwarp();
+    }
+    if (open[0] < 0 && open[1] < 0) return;
+    // The last CTA of a (sequence, unit) to arrive joins it.
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        const int i = threadIdx.x == 0 ? open[0] : open[1];
+        int last = 0;
+        if (i >= 0) {
+            // Releases what the CTA wrote before the barrier, and takes what
+            // the others released.
+            const int c0 = pieces[i].c0, more = pieces[i].c1 - c0;
+            unsigned* ticket = p.ctr + kPagedTickets + c0;
+            last = atom_add_acq_rel_gpu(ticket, 1u) == (unsigned)more;
+            if (last) *ticket = 0u;
+        }
+        misc[threadIdx.x] = last;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        if (!misc[part]) continue;
+        const PagedPiece& q = pieces[open[part]];
+        const int c0 = q.c0, c1 = q.c1;
+        const long long head0 = head_of(q.b, q.u);
+        for (int e = 4 * threadIdx.x; e < rows_of(q.u) * D; e += 4 * C::kThreads) {
+            const int r = e / D;
+            PagedSum sum;
+            constexpr int kAhead = 8;  // partials on their way together
+            for (int c = c0; c <= c1; c += kAhead) {
+                float m[kAhead], l[kAhead];
+                float4 o[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (c + k > c1) break;
+                    const float* at = p.part + ((long long)(c + k) * 2 + (c + k == c0)) * C::PART;
+                    m[k] = __ldcg(at + r);
+                    l[k] = __ldcg(at + kHeadRows + r);
+                    o[k] = __ldcg(reinterpret_cast<const float4*>(at + 2 * kHeadRows + e));
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (c + k > c1) break;
+                    sum.add(m[k], l[k], o[k]);
                 }
             }
-            __syncthreads();
+            sum.write<D>(p, head0, e);
         }
-        i = k;
     }
 }
 
