@@ -347,6 +347,8 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
     p.page_size = cache->page_size;
     p.n_pages = cache->n_pages;
     p.cap = table_tokens(max_pages, cache->page_size);
+    // The running sums of a batch's tiles are 32-bit.
+    if ((int64_t)batch * (p.cap / kTile + 2) >= (1ll << 31)) return ALSPEC_ERR_UNSUPPORTED;
     // No sequence is longer than cap, so neither term says more.
     p.S = std::min(n_sink, p.cap);
     p.W = std::min(window, p.cap);

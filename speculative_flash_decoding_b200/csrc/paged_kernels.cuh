@@ -345,47 +345,77 @@ struct PagedPos {
     PagedSeq s;
 };
 
-// The place of tile x (0 <= x < total) in the numbering (sequence, unit,
-// tile); called by a whole warp.
-__device__ __forceinline__ PagedPos paged_find(const PagedParams& p, long long x) {
+// The batch's tiles: lane i of a warp holds sequences [i * chunk, (i + 1) *
+// chunk), their tiles and the running sum up to their end.
+struct PagedBatch {
+    int chunk, n, incl;
+    int len;          // of the lane's sequence, with chunk 1
+    int units;
+    long long total;  // tiles of all sequences and units
+};
+
+__device__ __forceinline__ int warp_inclusive(int x) {
     const int lane = threadIdx.x & 31;
-    const int units = p.hkv * p.blocks;
-    long long base = 0;
-    PagedPos r;
-    r.b = r.u = r.i = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int n = b < p.batch ? paged_seq(p, __ldg(p.lens + b)).n : 0;
-        long long incl = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, (base + incl) * units > x);
-        if (past) {
-            const int w = __ffs(past) - 1;
-            const int nw = __shfl_sync(0xffffffffu, n, w);
-            const long long before = base + __shfl_sync(0xffffffffu, incl, w) - nw;
-            const unsigned off = (unsigned)(x - before * units);
-            r.b = b0 + w;
-            r.u = off / (unsigned)nw;
-            r.i = off % (unsigned)nw;
-            break;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
     }
-    r.s = paged_seq(p, __ldg(p.lens + r.b));
-    return r;
+    return x;
 }
 
-__device__ __forceinline__ long long paged_total(const PagedParams& p) {
-    long long n = 0;
+__device__ __forceinline__ PagedBatch paged_batch(const PagedParams& p) {
+    const int lane = threadIdx.x & 31;
+    PagedBatch s;
+    s.chunk = (p.batch + 31) / 32;
+    s.units = p.hkv * p.blocks;
+    s.n = s.len = 0;
 #pragma unroll 4
-    for (int b = threadIdx.x & 31; b < p.batch; b += 32) n += paged_seq(p, __ldg(p.lens + b)).n;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n * (p.hkv * p.blocks);
+    for (int b = lane * s.chunk; b < min(p.batch, (lane + 1) * s.chunk); ++b) {
+        s.len = __ldg(p.lens + b);
+        s.n += paged_seq(p, s.len).n;
+    }
+    s.incl = warp_inclusive(s.n);
+    s.total = (long long)__shfl_sync(0xffffffffu, s.incl, 31) * s.units;
+    return s;
+}
+
+// The place of tile x (0 <= x < total) in the numbering (sequence, unit,
+// tile); called by a whole warp.
+__device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const PagedBatch& t,
+                                               long long x) {
+    const int lane = threadIdx.x & 31;
+    PagedPos r;
+    const int w = __ffs(__ballot_sync(0xffffffffu, (long long)t.incl * t.units > x)) - 1;
+    int n = __shfl_sync(0xffffffffu, t.n, w);
+    long long before = __shfl_sync(0xffffffffu, t.incl, w) - n;
+    r.b = w;
+    if (t.chunk == 1) {
+        r.s = paged_seq(p, __shfl_sync(0xffffffffu, t.len, w));
+    } else {
+        // The same among the sequences of that lane.
+        for (int b0 = w * t.chunk;; b0 += 32) {
+            const int b = b0 + lane;
+            const bool in = b < min(p.batch, (w + 1) * t.chunk);
+            const int m = in ? paged_seq(p, __ldg(p.lens + b)).n : 0;
+            const int incl = warp_inclusive(m);
+            const unsigned past =
+                __ballot_sync(0xffffffffu, (before + incl) * t.units > x);
+            if (past || b0 + 32 >= (w + 1) * t.chunk) {
+                const int v = past ? __ffs(past) - 1 : 0;
+                n = __shfl_sync(0xffffffffu, m, v);
+                before += __shfl_sync(0xffffffffu, incl, v) - n;
+                r.b = b0 + v;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        r.s = paged_seq(p, __ldg(p.lens + r.b));
+    }
+    const unsigned off = (unsigned)(x - before * t.units);
+    r.u = (int)(off / (unsigned)n);
+    r.i = (int)(off % (unsigned)n);
+    return r;
 }
 
 // Shares: the tiles are spread over `workers` warps, warp w owning
@@ -431,15 +461,26 @@ struct PagedSum {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 
-    __device__ __forceinline__ void add(float pm, float pl, const float4& v) {
-        const float M = fmaxf(m, pm);
-        const float f = merge_weight(m, M), g = merge_weight(pm, M);
+    // N more partials at once: their weights do not wait for one another.
+    template <int N>
+    __device__ __forceinline__ void add(const float (&pm)[N], const float (&pl)[N],
+                                        const float4 (&v)[N]) {
+        float M = m;
+#pragma unroll
+        for (int k = 0; k < N; ++k) M = fmaxf(M, pm[k]);
+        const float f = m == M ? 1.f : fast_exp2(m - M);
         m = M;
-        l = l * f + pl * g;
-        o.x = o.x * f + v.x * g;
-        o.y = o.y * f + v.y * g;
-        o.z = o.z * f + v.z * g;
-        o.w = o.w * f + v.w * g;
+        l *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float g = pm[k] == M ? 1.f : fast_exp2(pm[k] - M);
+            l = fmaf(pl[k], g, l);
+            o.x = fmaf(v[k].x, g, o.x);
+            o.y = fmaf(v[k].y, g, o.y);
+            o.z = fmaf(v[k].z, g, o.z);
+            o.w = fmaf(v[k].w, g, o.w);
+        }
     }
     // Elements e .. e + 3 of the rows of D elements from head `head0` on.
     template <int D>
@@ -835,7 +876,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     pdl_wait_prerequisite();
     pdl_launch_dependents();
 
-    const long long total = paged_total(p);
+    const PagedBatch batch = paged_batch(p);
+    const long long total = batch.total;
     const long long workers = min((long long)gridDim.x * C::NW, total);
     const long long w = (long long)blockIdx.x * C::NW + warp;
     const long long x0 = w < workers ? share_begin(total, workers, w) : 0;
@@ -857,7 +899,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     };
 
     if (tiles > 0) {
-        PagedPos pos = paged_find(p, x0);
+        PagedPos pos = paged_find(p, batch, x0);
         const PagedPos start = pos;
         const uint64_t pol = p.blocks == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
         // A tile comes in boxes of `box` rows, K's and V's; lane i keeps the
@@ -936,7 +978,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         PagedSeq s = start.s;
         {
             // What this warp leaves to be joined, and with which CTAs.
-            const PagedPos end = paged_find(p, x0 + tiles - 1);
+            const PagedPos end = paged_find(p, batch, x0 + tiles - 1);
             auto piece = [&](PagedPiece& q, const PagedPos& at, long long tile0, int lo, int hi) {
                 q.b = at.b, q.u = at.u, q.n = at.s.n, q.lo = lo, q.hi = hi;
                 q.c0 = (int)(share_of(total, workers, tile0) / C::NW);
@@ -1058,10 +1100,11 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         return (long long)b * p.hq + (u / p.blocks) * p.group + (u % p.blocks) * kHeadRows;
     };
     // A run that began in an earlier CTA is this CTA's first partial, one that
-    // goes on in the next its second.  Runs go round the warps.
+    // goes on in the next its second.  The 128-element parts of all runs go
+    // round the warps.
     int open[2] = {-1, -1};  // the pieces that begin them
     int turn = 0;
-    for (unsigned left = starts; left; left &= left - 1, ++turn) {
+    for (unsigned left = starts; left; left &= left - 1) {
         const int i = __ffs(left) - 1;
         const unsigned next = left & (left - 1);
         const unsigned run = there & ~((1u << i) - 1u) & (next ? (next & -next) - 1u : ~0u);
@@ -1070,20 +1113,30 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         const bool whole = lo == 0 && hi == __shfl_sync(0xffffffffu, a.n, i);
         const int part = lo == 0 ? 1 : 0;
         if (!whole) open[part] = i;
-        if (turn % C::NW != warp) continue;
         const int b = __shfl_sync(0xffffffffu, a.b, i), u = __shfl_sync(0xffffffffu, a.u, i);
-        const long long head0 = head_of(b, u);
+        const int size = rows_of(u) * D;
         float* mine = p.part + ((long long)blockIdx.x * 2 + part) * C::PART;
-        for (int e = 4 * lane; e < rows_of(u) * D; e += 128) {
-            const int r = e / D;
+        for (int e0 = 0; e0 < size; e0 += 128, turn = turn + 1 == C::NW ? 0 : turn + 1) {
+            const int e = e0 + 4 * lane, r = e / D;
+            if (turn != warp || e >= size) continue;
             PagedSum sum;
-            for (unsigned k = run; k; k &= k - 1) {
-                const float* q = partial(__ffs(k) - 1);
-                sum.add(q[r], q[kHeadRows + r],
-                        *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e));
+            constexpr int kAhead = 4;  // partials on their way together
+            for (unsigned k = run; k;) {
+                float m[kAhead], l[kAhead];
+                float4 o[kAhead];
+#pragma unroll
+                for (int n = 0; n < kAhead; ++n) {
+                    const float* q = partial(k ? __ffs(k) - 1 : i);
+                    m[n] = k ? q[r] : -INFINITY;
+                    l[n] = k ? q[kHeadRows + r] : 0.f;
+                    o[n] = k ? *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                    k &= k - 1;
+                }
+                sum.add(m, l, o);
             }
             if (whole) {
-                sum.write<D>(p, head0, e);
+                sum.write<D>(p, head_of(b, u), e);
             } else {
                 __stcg(reinterpret_cast<float4*>(mine + 2 * kHeadRows + e), sum.o);
                 if (e % D == 0) {
@@ -1126,17 +1179,16 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                 float4 o[kAhead];
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    if (c + k > c1) break;
-                    const float* at = p.part + ((long long)(c + k) * 2 + (c + k == c0)) * C::PART;
-                    m[k] = __ldcg(at + r);
-                    l[k] = __ldcg(at + kHeadRows + r);
-                    o[k] = __ldcg(reinterpret_cast<const float4*>(at + 2 * kHeadRows + e));
+                    m[k] = -INFINITY, l[k] = 0.f, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + k <= c1) {
+                        const float* at =
+                            p.part + ((long long)(c + k) * 2 + (c + k == c0)) * C::PART;
+                        m[k] = __ldcg(at + r);
+                        l[k] = __ldcg(at + kHeadRows + r);
+                        o[k] = __ldcg(reinterpret_cast<const float4*>(at + 2 * kHeadRows + e));
+                    }
                 }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (c + k > c1) break;
-                    sum.add(m[k], l[k], o[k]);
-                }
+                sum.add(m, l, o);
             }
             sum.write<D>(p, head0, e);
         }
