@@ -288,18 +288,14 @@ struct PagedCfg {
     static constexpr int SEG = BOX * SEGB;                // one segment of a box
     static constexpr int TILEB = kTile * RB;              // K or V of a tile
     static constexpr int STAGEB = 2 * TILEB;
-    // Warps, and stages per warp, of a 192 KB ring.
-#ifndef NW16
-#define NW16 6
-#endif
-#ifndef NW8
-#define NW8 8
-#endif
-#ifndef NW4
-#define NW4 16
-#endif
-    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? NW16 : STAGEB >= 8192 ? NW8 : NW4;
-    static constexpr int ST = 196608 / STAGEB / NW;
+    // Warps, and two stages each.  128 KB on their way keep HBM busy; 192 KB
+    // made the SMs unequal (128K tokens of bf16: some CTAs done after 60 us,
+    // some after 85; 87.6 us a call against 84.2, 30000 x 8 of 64 bf16
+    // elements 87.2 against 81.0), 96 KB took 90.4 us.  fp32 pages cost more
+    // instructions a byte: as many warps as fit.
+    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? (T == kPagesF32 ? 6 : 4)
+                              : STAGEB >= 8192 ? 8 : 16;
+    static constexpr int ST = 2;
     static constexpr int kThreads = NW * 32;
     // Offset of a row (a multiple of 8, or its row within 8 added later).
     __host__ __device__ static constexpr int row(int r) {
@@ -682,7 +678,10 @@ struct PagedWarp {
         for (int n = 0; n < 4; ++n) mx = fmaxf(mx, fmaxf(x[n][0], x[n][1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * f;
-        const float m_new = fmaxf(m, mx);
+        // The reference of the exponentials follows the maximum only when it
+        // is 2^8 behind: until then weights of up to 2^8 do no harm, and the
+        // sums need no rescaling.
+        const float m_new = mx > m + 8.f ? mx : m;
         const float base = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = m == m_new ? 1.f : fast_exp2(m - base);
         float rescale = alpha, vinv = 1.f;
