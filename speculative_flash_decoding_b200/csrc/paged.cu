@@ -84,6 +84,22 @@ int table_tokens(int max_pages, int page_size) {
     return (int)std::min<long long>((long long)max_pages * page_size, (1ll << 31) - 4096);
 }
 
+// A programmatic launch: every kernel of this file waits for the kernel ahead
+// before it touches memory.
+template <typename P>
+alspec_status launch(void (*fn)(P), unsigned blocks, unsigned threads, int smem, void* stream,
+                     const P& p) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr = programmatic_launch();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return ok(cudaLaunchKernelEx(&cfg, fn, p)) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
+}
+
 // ------------------------------------------------------------ append, gather
 
 using AppendFn = void (*)(AppendParams);
@@ -237,9 +253,11 @@ alspec_status alspec_paged_append(const alspec_paged_cache* cache, const void* k
             return ALSPEC_ERR_INVALID_ARG;
         p.src_stride[w] = s ? s : row;
     }
-    const int64_t threads = (int64_t)n_tokens * cache->n_kv_heads * (cache->head_dim / 8);
-    const int64_t blocks = (threads + kAppendThreads - 1) / kAppendThreads;
-    if (blocks > 0x7fffffff) return ALSPEC_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)n_tokens * cache->n_kv_heads;
+    if (rows > 0x40000000) return ALSPEC_ERR_UNSUPPORTED;
+    const int per_block = kAppendThreads / (cache->head_dim / kAppendLane);
+    const int64_t blocks = std::min<int64_t>((rows + per_block - 1) / per_block,
+                                             (int64_t)kAppendCtas * sm_count_for_plan());
     p.lay = layout_of(*cache);
     p.pages[0] = cache->k_pages;
     p.pages[1] = cache->v_pages;
@@ -256,8 +274,7 @@ alspec_status alspec_paged_append(const alspec_paged_cache* cache, const void* k
     p.err = err;
     const AppendFn fn = cache->head_dim == 128 ? append_for<128>(src_dtype, cache->dtype)
                                                : append_for<64>(src_dtype, cache->dtype);
-    fn<<<(unsigned)blocks, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return ok(cudaGetLastError()) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
+    return launch(fn, (unsigned)blocks, kAppendThreads, 0, stream, p);
 }
 
 alspec_status alspec_paged_gather(const alspec_paged_cache* cache, const int32_t* page_table,
@@ -291,8 +308,7 @@ alspec_status alspec_paged_gather(const alspec_paged_cache* cache, const int32_t
     p.err = err;
     const GatherFn fn = cache->head_dim == 128 ? gather_for<128>(cache->dtype, out_dtype)
                                                : gather_for<64>(cache->dtype, out_dtype);
-    fn<<<(unsigned)blocks, kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return ok(cudaGetLastError()) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
+    return launch(fn, (unsigned)blocks, kGatherThreads, 0, stream, p);
 }
 
 size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, int n_q_heads) {
@@ -373,15 +389,7 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
     p.heads = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(ctas) +
                                        part_bytes(kern, ctas));
     p.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3((unsigned)kern.threads);
-    cfg.dynamicSmemBytes = kern.smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr = programmatic_launch();
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return ok(cudaLaunchKernelEx(&cfg, kern.fn, p)) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
+    return launch(kern.fn, (unsigned)ctas, (unsigned)kern.threads, kern.smem, stream, p);
 }
 
 }  // extern "C"

@@ -32,25 +32,34 @@ struct PageLayout {
     }
 };
 
-// Eight values as fp32, from fp32 or bf16 (16-byte aligned).
+// Eight values as they lie, fp32 or bf16 (16-byte aligned), and as fp32.
 template <int T>
-__device__ __forceinline__ void load8(const void* base, long long i, float (&x)[8]) {
-    if constexpr (T == kF32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 r = __ldg(
-            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i));
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw8 {
+    uint4 r[T == kF32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void* base, long long i) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) +
+                                                        i * (T == kF32 ? 4 : 2));
+        r[0] = __ldg(p);
+        if constexpr (T == kF32) r[1] = __ldg(p + 1);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+        const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            if constexpr (T == kF32) {
+                x[j] = __uint_as_float(w[j]);
+            } else {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+        if constexpr (T == kF32) {
+            x[4] = __uint_as_float(r[1].x), x[5] = __uint_as_float(r[1].y);
+            x[6] = __uint_as_float(r[1].z), x[7] = __uint_as_float(r[1].w);
         }
     }
-}
+};
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -87,63 +96,149 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 6;  // CTAs for each SM, at most
 
-// D / 8 lanes hold one (token, KV head)'s row of K and of V, eight values
-// each, so every access is 8 to 32 bytes wide and amax is a few shuffles;
-// the source rows are loaded before the positions and the table have come
-// back.  Bound by latency for a decode step and by bytes for a prompt.
+// Two quotients x / s correctly rounded, from r = 1 / s rounded: the remainder
+// of the product is exact, and one more step with it rounds right (P.
+// Markstein, Computation of elementary functions on the IBM RISC System/6000,
+// 1990).  Holds where nothing underflows; append takes it for scales away
+// from the ends of the range.
+__device__ __forceinline__ float2 quotients(float2 x, float s, float r) {
+    const float2 rr = make_float2(r, r);
+    const float2 q = __fmul2_rn(x, rr);
+    return __ffma2_rn(__ffma2_rn(make_float2(-q.x, -q.y), make_float2(s, s), x), rr, q);
+}
+
+// The larger of two pairs of unsigned 16-bit integers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// D / 16 lanes hold one (token, KV head)'s row of K and of V, sixteen values
+// each, so every access is 16 bytes wide and amax is a few shuffles.  A
+// thread goes from row to row with the next row's values and position on
+// their way.  Bound by latency for a decode step; for a prompt by bytes and,
+// quantising, by instructions: amax runs on pairs of bf16 magnitudes as
+// integers, the division is a product and two fused steps on pairs (with
+// eight values a lane and one division each, 16411 tokens of 8 heads took
+// 29.1 us).
+constexpr int kAppendLane = 16;  // values of a lane
+
+template <int SRC>
+struct AppendRow {
+    Raw8<SRC> x[2][2];
+    int t, h, pos, seq;
+
+    template <int D>
+    __device__ __forceinline__ void load(const AppendParams& p, unsigned row, unsigned rows,
+                                         int col) {
+        pos = -1;
+        if (row >= rows) return;
+        t = (int)(row / (unsigned)p.lay.hkv);
+        h = (int)(row - (unsigned)t * (unsigned)p.lay.hkv);
+        pos = __ldg(p.positions + t);
+        seq = p.seq_ids ? __ldg(p.seq_ids + t) : t;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                x[w][i].load(p.src[w], t * p.src_stride[w] + (long long)h * D + col + 8 * i);
+    }
+
+    // Largest magnitude of this lane's values as the bits of an fp32: NaN is
+    // above infinity, so either one makes the scale, and with it the row, not
+    // finite.
+    __device__ __forceinline__ uint32_t largest(int w) const {
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < (SRC == kF32 ? 2 : 1); ++j) {
+                const uint4& r = x[w][i].r[j];
+                if constexpr (SRC == kF32) {
+                    a = max(a, max(max(r.x & 0x7fffffffu, r.y & 0x7fffffffu),
+                                   max(r.z & 0x7fffffffu, r.w & 0x7fffffffu)));
+                } else {
+                    a = max_u16x2(a, max_u16x2(max_u16x2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu),
+                                               max_u16x2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu)));
+                }
+            }
+        return SRC == kF32 ? a : max(a & 0xffff0000u, a << 16);
+    }
+};
+
 template <int SRC, int DST, int D>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(
     const __grid_constant__ AppendParams p) {
-    constexpr int LPR = D / 8;  // lanes per row
-    const long long idx = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-    const long long pair = idx / LPR;  // (token, head)
-    const int col = (int)(idx % LPR) * 8;
-    const bool live = pair < (long long)p.n * p.lay.hkv;
-    const int t = live ? (int)(pair / p.lay.hkv) : 0;
-    const int h = live ? (int)(pair % p.lay.hkv) : 0;
-    float x[2][8];
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-        load8<SRC>(p.src[w], t * p.src_stride[w] + (long long)h * D + col, x[w]);
-    const int pos = __ldg(p.positions + t);
-    const int seq = p.seq_ids ? __ldg(p.seq_ids + t) : t;
-    int page = -1;
-    if (live && pos >= 0) {
-        const int entry = pos / p.lay.page_size;
-        if (seq >= 0 && seq < p.batch && entry < p.max_pages)
-            page = __ldg(p.table + (long long)seq * p.max_pages + entry);
-        if (page < 0 || page >= p.lay.n_pages) {
-            page = -1;
-            if (p.err && col == 0) atomicOr(p.err, kErrPage);
-        }
-    }
-    const int slot = pos >= 0 ? pos % p.lay.page_size : 0;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        if constexpr (DST == kE4m3) {
-            // amax as an integer maximum of magnitudes: NaN is above
-            // infinity, so either one makes the scale, and with it the row,
-            // not finite.
-            uint32_t a = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[w][j]) & 0x7fffffffu);
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-            float s = __fdiv_rn(__uint_as_float(a), kE4m3Max);
-            s = s < kMinScale ? kMinScale : s;
-            uint32_t c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[j] = f32x2_to_e4m3x2(__fdiv_rn(x[w][2 * j], s), __fdiv_rn(x[w][2 * j + 1], s));
-            if (page >= 0) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.pages[w]) +
-                                          p.lay.row(page, h, slot) + col) =
-                    make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-                if (col == 0) p.scales[w][p.lay.scale(page, h, slot)] = s;
+    constexpr int LPR = D / kAppendLane;  // lanes per row
+    pdl_wait_prerequisite();
+    pdl_launch_dependents();
+    const unsigned rows = (unsigned)p.n * (unsigned)p.lay.hkv;
+    const unsigned step = gridDim.x * (kAppendThreads / LPR);
+    const int col = (int)(threadIdx.x % LPR) * kAppendLane;
+    AppendRow<SRC> next;
+    unsigned row = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
+    next.template load<D>(p, row, rows, col);
+    // A whole CTA makes the same number of rounds.
+    for (unsigned base = blockIdx.x * (kAppendThreads / LPR); base < rows;
+         base += step, row += step) {
+        const AppendRow<SRC> cur = next;
+        int page = -1, slot = 0;
+        if (cur.pos >= 0) {
+            const unsigned entry = (unsigned)cur.pos / (unsigned)p.lay.page_size;
+            slot = cur.pos - (int)entry * p.lay.page_size;
+            if (cur.seq >= 0 && cur.seq < p.batch && entry < (unsigned)p.max_pages)
+                page = __ldg(p.table + (long long)cur.seq * p.max_pages + entry);
+            if (page < 0 || page >= p.lay.n_pages) {
+                page = -1;
+                if (p.err && col == 0) atomicOr(p.err, kErrPage);
             }
-        } else if (page >= 0) {
-            store8<DST>(p.pages[w], p.lay.row(page, h, slot) + col, x[w]);
+        }
+        if (base + step < rows) next.template load<D>(p, row + step, rows, col);
+        const long long at = p.lay.row(page, cur.h, slot) + col;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float x[2][8];
+            cur.x[w][0].unpack(x[0]);
+            cur.x[w][1].unpack(x[1]);
+            if constexpr (DST == kE4m3) {
+                uint32_t a = cur.largest(w);
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1)
+                    a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+                float s = __fdiv_rn(__uint_as_float(a), kE4m3Max);
+                s = s < kMinScale ? kMinScale : s;
+                uint32_t c[4];
+                if (s > 1e-30f && s < 1e36f) {
+                    const float r = __frcp_rn(s);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 q = quotients(
+                            make_float2(x[j / 4][2 * j % 8], x[j / 4][2 * j % 8 + 1]), s, r);
+                        const uint32_t two = f32x2_to_e4m3x2(q.x, q.y);
+                        c[j / 2] = j % 2 ? c[j / 2] | two << 16 : two;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t two =
+                            f32x2_to_e4m3x2(__fdiv_rn(x[j / 4][2 * j % 8], s),
+                                            __fdiv_rn(x[j / 4][2 * j % 8 + 1], s));
+                        c[j / 2] = j % 2 ? c[j / 2] | two << 16 : two;
+                    }
+                }
+                __syncwarp();
+                if (page >= 0) {
+                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.pages[w]) + at) =
+                        make_uint4(c[0], c[1], c[2], c[3]);
+                    if (col == 0) p.scales[w][p.lay.scale(page, cur.h, slot)] = s;
+                }
+            } else if (page >= 0) {
+                store8<DST>(p.pages[w], at, x[0]);
+                store8<DST>(p.pages[w], at + 8, x[1]);
+            }
         }
     }
 }
@@ -171,6 +266,8 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
     const __grid_constant__ GatherParams p) {
     constexpr int LPR = D / 8;
     constexpr int RPI = kGatherThreads / LPR;  // rows per iteration
+    pdl_wait_prerequisite();
+    pdl_launch_dependents();
     const unsigned bh = blockIdx.x / p.blocks_per_head;
     const int t0 = (int)(blockIdx.x % p.blocks_per_head) * kGatherRows;
     const int b = bh / p.lay.hkv, h = bh % p.lay.hkv;
@@ -209,7 +306,9 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
                     x[2 * j + 1] = v.y * s;
                 }
             } else {
-                load8<SRC>(p.pages[w], src, x);
+                Raw8<SRC> raw;
+                raw.load(p.pages[w], src);
+                raw.unpack(x);
             }
             store8<DST>(p.out[w], dst, x);
         }
@@ -631,10 +730,12 @@ struct PagedWarp {
                     mma_bf16_16816(s[n], qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, f[2], f[3]);
                 } else if constexpr (T == kPagesE4m3) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t b0, b1;
+                        e4m3x4_to_f16x4(f[i], b0, b1);
                         mma_f16_16816(s[n], qa[c + i][0], qb[c + i][0], qa[c + i][1], qb[c + i][1],
-                                      e4m3x2_to_f16x2((uint16_t)f[i]),
-                                      e4m3x2_to_f16x2((uint16_t)(f[i] >> 16)));
+                                      b0, b1);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -768,14 +869,11 @@ struct PagedWarp {
                         // the even and the odd column's tokens.
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
-                            const uint32_t g0 = __byte_perm(f4[2 * w], 0u, 0x3120);
-                            const uint32_t g1 = __byte_perm(f4[2 * w + 1], 0u, 0x3120);
-                            mma_f16_16816(acc[2 * (c + w)], a[0], a[1], a[2], a[3],
-                                          e4m3x2_to_f16x2((uint16_t)g0),
-                                          e4m3x2_to_f16x2((uint16_t)g1));
-                            mma_f16_16816(acc[2 * (c + w) + 1], a[0], a[1], a[2], a[3],
-                                          e4m3x2_to_f16x2((uint16_t)(g0 >> 16)),
-                                          e4m3x2_to_f16x2((uint16_t)(g1 >> 16)));
+                            uint32_t even0, odd0, even1, odd1;
+                            e4m3x4_to_f16x4(__byte_perm(f4[2 * w], 0u, 0x3120), even0, odd0);
+                            e4m3x4_to_f16x4(__byte_perm(f4[2 * w + 1], 0u, 0x3120), even1, odd1);
+                            mma_f16_16816(acc[2 * (c + w)], a[0], a[1], a[2], a[3], even0, even1);
+                            mma_f16_16816(acc[2 * (c + w) + 1], a[0], a[1], a[2], a[3], odd0, odd1);
                         }
                     } else {
                         mma_bf16_16816(acc[c], a[0], a[1], a[2], a[3], f4[0], f4[1]);
