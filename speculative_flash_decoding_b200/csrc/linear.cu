@@ -75,10 +75,11 @@ bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
 }
 
 // CTAs that share the K of a tile: the number that makes (waves of clusters)
-// x (blocks of a CTA, plus four for the exchange where there is one)
-// smallest.  Clusters leave SMs idle (148 SMs hold 74 pairs, but 45 clusters
-// of 3, 33 of 4, 15 of 7 or 8), and a second wave costs more than an idle SM:
-// 33 x 4096 x 6144 (48 tiles) takes 24 us with 3 and 15.0 with 2.
+// x (blocks of a CTA, plus 16 for a wave's beginning and end and four for the
+// exchange where there is one) smallest.  Clusters leave SMs idle (148 SMs
+// hold 74 pairs, but 45 clusters of 3, 33 of 4, 26 of 5, 15 of 8), and a
+// second wave costs more than idle SMs: 33 x 4096 x 6144 (48 tiles) takes 24
+// us with 3, 19.6 with 5 and 15 with 2.
 int choose_split(int64_t tiles, int kblocks) {
     int n[kLinMaxSplit + 1];
     if (!resident_clusters(n)) return 0;
@@ -86,7 +87,7 @@ int choose_split(int64_t tiles, int kblocks) {
     int64_t least = INT64_MAX;
     for (int c = 1; c <= kLinMaxSplit && c <= std::max(1, kblocks / 4); ++c) {
         const int64_t waves = (tiles + n[c] - 1) / n[c];
-        const int64_t cost = waves * ((kblocks + c - 1) / c + (c > 1 ? 4 : 0));
+        const int64_t cost = waves * ((kblocks + c - 1) / c + (c > 1 ? 20 : 16));
         if (cost < least) least = cost, best = c;
     }
     return best;

@@ -110,7 +110,9 @@ __device__ __forceinline__ void lin_load16(uint32_t addr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The activation of N sums: one branch on its kind, not one per sum.
+// The activation of N sums: one branch on its kind, not one per sum.  SiLU
+// takes the fast exponential and quotient (a few units of 2^-23 of the
+// result, times |x| where it is far below zero).
 template <int N>
 __device__ __forceinline__ void lin_activate(float (&x)[N], int act) {
     if (act == 1) {
@@ -121,7 +123,7 @@ __device__ __forceinline__ void lin_activate(float (&x)[N], int act) {
         for (int i = 0; i < N; ++i) x[i] = 0.5f * x[i] * (1.f + erff(x[i] * 0.70710678118654752f));
     } else if (act == 3) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = x[i] / (1.f + expf(-x[i]));
+        for (int i = 0; i < N; ++i) x[i] = __fdividef(x[i], 1.f + __expf(-x[i]));
     }
 }
 
@@ -153,8 +155,8 @@ __device__ __forceinline__ void lin_put4(__nv_bfloat16* p, const float* v) {
 constexpr int kLinRows = 4;
 
 template <typename O>
-__device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int c0, int c1,
-                                             int r0, int n0) {
+__device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int rank,
+                                             int c0, int c1, int r0, int n0) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kWarps = kLinThreads / 32;
     const int f = n0 + 4 * lane;
@@ -185,12 +187,20 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
                 }
             }
         }
+        const uint32_t here = sums + (uint32_t)(c * kLinM + 4 * lane) * 4;
         for (int s = 0; s < p.split; ++s) {
-            const uint32_t from = dsmem_addr(sums + (uint32_t)(c * kLinM + 4 * lane) * 4, s);
+            // This CTA's own part without the way through the cluster.
             float4 part[kLinRows];
+            if (s == rank) {
 #pragma unroll
-            for (int u = 0; u < kLinRows; ++u)
-                if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
+                for (int u = 0; u < kLinRows; ++u)
+                    if (c + u * kWarps < c1) part[u] = lds_v4(here + u * kWarps * kLinM * 4);
+            } else {
+                const uint32_t from = dsmem_addr(here, s);
+#pragma unroll
+                for (int u = 0; u < kLinRows; ++u)
+                    if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
+            }
 #pragma unroll
             for (int u = 0; u < kLinRows; ++u) {
                 v[4 * u] = s ? v[4 * u] + part[u].x : part[u].x;
@@ -370,9 +380,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         __syncthreads();
     if (good) {
         if (p.out_bf16)
-            lin_epilogue<__nv_bfloat16>(p, smem_addr(mine), c0, c1, r0, n0);
+            lin_epilogue<__nv_bfloat16>(p, smem_addr(mine), rank, c0, c1, r0, n0);
         else
-            lin_epilogue<float>(p, smem_addr(mine), c0, c1, r0, n0);
+            lin_epilogue<float>(p, smem_addr(mine), rank, c0, c1, r0, n0);
     }
     if (p.split > 1) cluster_sync();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
