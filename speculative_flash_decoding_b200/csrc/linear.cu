@@ -49,7 +49,7 @@ std::mutex g_clusters_mutex;
 bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
     int dev = 0;
     if (!ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return false;
-    if (smem_attr_once(reinterpret_cast<const void*>(linear_kernel), kLinRing + 1024) != ALSPEC_OK)
+    if (smem_attr_once(reinterpret_cast<const void*>(linear_kernel), kLinSmem) != ALSPEC_OK)
         return false;
     std::lock_guard<std::mutex> lock(g_clusters_mutex);
     int(&n)[kLinMaxSplit + 1] = g_clusters[dev];
@@ -57,7 +57,7 @@ bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)c);
         cfg.blockDim = dim3(kLinThreads);
-        cfg.dynamicSmemBytes = kLinRing + 1024;
+        cfg.dynamicSmemBytes = kLinSmem;
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = c;
@@ -129,16 +129,22 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     if (tiles * p.split > 0x7fffffff || n > 0x7fffffff - kLinM) return ALSPEC_ERR_UNSUPPORTED;
     // Blocks of a stage: four (512 consecutive bytes of a row of W) where the
     // ring holds two such stages, else two.  DRAM wants neighbouring columns
-    // asked for together: one block a stage, the ring as large, took 35.1 us
+    // asked for together: one block a stage, a ring of 200 KB, took 35.1 us
     // for 16 x 8192 x 8192, two 26.4, four 26.9; for 33 x 4096 x 6144 two 16.0,
     // four 15.0.
-    p.group = (kLinM + p.nt) * 128 * 8 <= kLinRing ? 4 : 2;
+    const int rows_tile = std::min(p.nt, rows);
+    p.push = p.nt <= kLinPush;
+    p.slice = (rows_tile + p.split - 1) / p.split;
+    const int exchange = p.push ? p.split * p.slice * kLinM * 4 : 0;
+    const int ring = kLinSmem - 1024 - exchange;
+    p.group = (kLinM + p.nt) * 128 * 8 <= ring ? 4 : 2;
     const int stage = (kLinM + p.nt) * 128 * p.group;
     const int fills = ((p.kblocks + p.split - 1) / p.split + p.group - 1) / p.group;
-    p.stages = std::min({kLinMaxStages, kLinRing / stage, std::max(2, fills)});
+    p.stages = std::min({kLinMaxStages, ring / stage, std::max(2, fills)});
     p.tmem_cols = 32;
     while (p.tmem_cols < p.nt) p.tmem_cols *= 2;
-    const int smem = std::max({p.stages * stage, p.nt * kLinM * 4, kLinMinSmem}) + 1024;
+    const int smem =
+        std::max({p.stages * stage + exchange, p.push ? 0 : p.nt * kLinM * 4, kLinMinSmem}) + 1024;
     alspec_status st = encode_matrix(&p.tw, &p.tw_end, w, k, n, k, kLinM, p.group);
     if (st != ALSPEC_OK) return st;
     if ((st = encode_matrix(&p.tx, &p.tx_end, x, k, rows, x_stride ? x_stride : k, p.nt,
@@ -157,7 +163,7 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     p.err = err;
     p.timeout_ns = 2000000000ull;
     const void* fn = reinterpret_cast<const void*>(linear_kernel);
-    if ((st = smem_attr_once(fn, kLinRing + 1024)) != ALSPEC_OK) return st;
+    if ((st = smem_attr_once(fn, kLinSmem)) != ALSPEC_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
     cfg.blockDim = dim3(kLinThreads);

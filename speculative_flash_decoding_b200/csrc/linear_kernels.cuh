@@ -5,7 +5,7 @@
 // of a tcgen05.mma, up to 256 rows of x its N, and the accumulator is
 // y^T in TMEM (lane = feature, column = batch row).  W is read once from HBM
 // while x comes from L2; TMA brings 64-column slices of both (128-byte
-// swizzle) through a ring of up to 200 KB.  One warp's lane issues the
+// swizzle) through a ring of up to 220 KB.  One warp's lane issues the
 // copies, one the MMAs, then eight warps read the accumulator back for the
 // epilogue.  When there are fewer tiles than SMs, the CTAs of a cluster
 // split K and add their accumulators through distributed shared memory, each
@@ -28,8 +28,9 @@ constexpr int kLinM = 128;        // features per tile
 constexpr int kLinK = 64;         // columns of a stage: 128 bytes
 constexpr int kLinMaxN = 256;     // batch rows per tile
 constexpr int kLinMaxStages = 12;
-constexpr int kLinRing = 200 * 1024;
+constexpr int kLinSmem = 224 * 1024;  // dynamic shared memory, at most
 constexpr int kLinMaxSplit = 8;   // CTAs of a cluster
+constexpr int kLinPush = 48;      // batch rows of a small batch's tile, at most
 constexpr int kLinAhead = 8;      // blocks asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM
 // holds one CTA and its TMEM allocation never waits for another's.
@@ -49,6 +50,8 @@ struct LinearParams {
     int group;     // 64-column blocks a stage holds
     int tmem_cols;
     int out_bf16, act;
+    int push;      // parts of the sums go to the CTA that finishes their rows
+    int slice;     // batch rows that a CTA finishes, at most
     int vec;       // y and the residual can be taken four features at a time
     unsigned* err;
     unsigned long long timeout_ns;
@@ -148,13 +151,12 @@ __device__ __forceinline__ void lin_put4(__nv_bfloat16* p, const float* v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
-// The epilogue of batch rows [c0, c1) of a tile whose sums lie in shared
-// memory, [row][feature], one part in each of the cluster's CTAs.  A warp
-// takes a row at a time, a lane four features; everything a round of
-// kLinRows rows needs is asked for before it is used.
-constexpr int kLinRows = 4;
-
-template <typename O>
+// The epilogue of batch rows [c0, c1) of a tile.  Their sums lie in shared
+// memory, either one part in each of the cluster's CTAs, [row][feature], or
+// (PUSH) all parts here, [CTA][row - c0][feature].  A warp takes a row at a
+// time, a lane four features; everything a round of R rows needs is asked for
+// before it is used (rounds of four rows: 44.1 us for 250 x 8192 x 8192).
+template <typename O, bool PUSH, int R>
 __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int rank,
                                              int c0, int c1, int r0, int n0) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,14 +170,14 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
         for (int i = 0; i < 4; ++i)
             if (i < nf) bias[i] = __bfloat162float(p.bias[f + i]);
     }
-    for (int c = c0 + warp; c < c1; c += kWarps * kLinRows) {
+    for (int c = c0 + warp; c < c1; c += kWarps * R) {
         const long long at = (long long)(r0 + c) * p.n + f;
         const long long step = (long long)kWarps * p.n;
         const O* res = static_cast<const O*>(p.residual);
-        float v[4 * kLinRows], add[4 * kLinRows];
+        float v[4 * R], add[4 * R];
         if (res) {
 #pragma unroll
-            for (int u = 0; u < kLinRows; ++u) {
+            for (int u = 0; u < R; ++u) {
                 if (c + u * kWarps >= c1) continue;
                 if (p.vec) {
                     const float4 x = lin_value4(res + at + u * step);
@@ -187,22 +189,24 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
                 }
             }
         }
-        const uint32_t here = sums + (uint32_t)(c * kLinM + 4 * lane) * 4;
+        const uint32_t here =
+            sums + (uint32_t)((PUSH ? c - c0 : c) * kLinM + 4 * lane) * 4;
         for (int s = 0; s < p.split; ++s) {
             // This CTA's own part without the way through the cluster.
-            float4 part[kLinRows];
-            if (s == rank) {
+            float4 part[R];
+            if (PUSH || s == rank) {
+                const uint32_t from = here + (uint32_t)(PUSH ? s * p.slice * kLinM * 4 : 0);
 #pragma unroll
-                for (int u = 0; u < kLinRows; ++u)
-                    if (c + u * kWarps < c1) part[u] = lds_v4(here + u * kWarps * kLinM * 4);
+                for (int u = 0; u < R; ++u)
+                    if (c + u * kWarps < c1) part[u] = lds_v4(from + u * kWarps * kLinM * 4);
             } else {
                 const uint32_t from = dsmem_addr(here, s);
 #pragma unroll
-                for (int u = 0; u < kLinRows; ++u)
+                for (int u = 0; u < R; ++u)
                     if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
             }
 #pragma unroll
-            for (int u = 0; u < kLinRows; ++u) {
+            for (int u = 0; u < R; ++u) {
                 v[4 * u] = s ? v[4 * u] + part[u].x : part[u].x;
                 v[4 * u + 1] = s ? v[4 * u + 1] + part[u].y : part[u].y;
                 v[4 * u + 2] = s ? v[4 * u + 2] + part[u].z : part[u].z;
@@ -210,15 +214,15 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4 * kLinRows; ++i) v[i] += bias[i % 4];
+        for (int i = 0; i < 4 * R; ++i) v[i] += bias[i % 4];
         lin_activate(v, p.act);
         if (res) {
 #pragma unroll
-            for (int i = 0; i < 4 * kLinRows; ++i) v[i] += add[i];
+            for (int i = 0; i < 4 * R; ++i) v[i] += add[i];
         }
         O* y = static_cast<O*>(p.y);
 #pragma unroll
-        for (int u = 0; u < kLinRows; ++u) {
+        for (int u = 0; u < R; ++u) {
             if (c + u * kWarps >= c1) continue;
             if (p.vec) {
                 lin_put4(y + at + u * step, v + 4 * u);
@@ -236,6 +240,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     extern __shared__ unsigned char lin_raw[];
     __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], done;
     __shared__ uint32_t tmem_base;
+    __shared__ uint16_t owner[kLinPush];
     __shared__ int abort_flag;
     volatile int* abort = &abort_flag;
     unsigned char* ring = reinterpret_cast<unsigned char*>(
@@ -251,6 +256,12 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     const int fills = (kb1 - kb0 + p.group - 1) / p.group;
     const int rows = min(p.nt, p.rows - r0);
     const int c0 = rank * rows / p.split, c1 = (rank + 1) * rows / p.split;  // this CTA finishes
+    // Small batches: who finishes row c (low 4 bits), as which of its rows.
+    float* exchange = reinterpret_cast<float*>(ring + p.stages * stage_bytes);
+    if (p.push && (int)threadIdx.x < rows) {
+        const int c = (int)threadIdx.x, r = ((c + 1) * p.split - 1) / rows;
+        owner[c] = (uint16_t)(r | (c - r * rows / p.split) << 4);
+    }
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -289,6 +300,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     }
     pdl_wait_prerequisite();
     pdl_launch_dependents();
+    // Every CTA of the cluster has begun before one writes to another (waited
+    // for there).
+    if (p.push && p.split > 1) cluster_arrive_relaxed();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -361,30 +375,62 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     __syncthreads();
 
-    // This CTA's sums, [batch row][feature], go where the ring was (warp w
-    // reads the 32 lanes of its quarter, the two halves of the warps take
-    // alternate groups of 16 columns); then every CTA of the cluster finishes
-    // its share of the rows.
-    float* mine = reinterpret_cast<float*>(ring);
+    // Warp w reads the 32 lanes of its quarter, the two halves of the warps
+    // alternate groups of 16 columns.
     const int fl = (warp & 3) * 32 + lane;  // feature within the tile
     const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    for (int c = 16 * (warp >> 2); c < rows; c += 32) {
-        float v[16];
-        lin_load16(taddr + c, v);
+    if (p.push) {
+        // Small batches: a part goes straight to the CTA that finishes the
+        // row, into a buffer beside the ring, and one cluster barrier later
+        // every CTA is on its own.  (Reading the others' parts needs a second
+        // barrier before anyone may leave: 1 x 4096 x 4096 10.1 us.)
+        if (p.split > 1) cluster_wait();
+        const uint32_t mine =
+            smem_addr(exchange) + (uint32_t)(rank * p.slice * kLinM + fl) * 4;
+        for (int c = 16 * (warp >> 2); c < rows; c += 32) {
+            float v[16];
+            lin_load16(taddr + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + fl] = v[i];
-    }
-    if (p.split > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    if (good) {
-        if (p.out_bf16)
-            lin_epilogue<__nv_bfloat16>(p, smem_addr(mine), rank, c0, c1, r0, n0);
+            for (int i = 0; i < 16; ++i) {
+                if (c + i < rows) {
+                    const int to = owner[c + i] & 15, at = owner[c + i] >> 4;
+                    st_dsmem(dsmem_addr(mine + at * kLinM * 4, to), v[i]);
+                }
+            }
+            __syncwarp();
+        }
+        if (p.split > 1)
+            cluster_sync();
         else
-            lin_epilogue<float>(p, smem_addr(mine), rank, c0, c1, r0, n0);
+            __syncthreads();
+        if (good) {
+            if (p.out_bf16)
+                lin_epilogue<__nv_bfloat16, true, 2>(p, smem_addr(exchange), rank, c0, c1, r0, n0);
+            else
+                lin_epilogue<float, true, 2>(p, smem_addr(exchange), rank, c0, c1, r0, n0);
+        }
+    } else {
+        // Large batches: this CTA's parts, [batch row][feature], go where the
+        // ring was, and every CTA reads those of the rows it finishes.
+        float* mine = reinterpret_cast<float*>(ring);
+        for (int c = 16 * (warp >> 2); c < rows; c += 32) {
+            float v[16];
+            lin_load16(taddr + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + fl] = v[i];
+        }
+        if (p.split > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        if (good) {
+            if (p.out_bf16)
+                lin_epilogue<__nv_bfloat16, false, 8>(p, smem_addr(mine), rank, c0, c1, r0, n0);
+            else
+                lin_epilogue<float, false, 8>(p, smem_addr(mine), rank, c0, c1, r0, n0);
+        }
+        if (p.split > 1) cluster_sync();
     }
-    if (p.split > 1) cluster_sync();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (warp == 2)

@@ -170,19 +170,13 @@ PagedKernel paged_kernel_for(const alspec_paged_cache& c, int out_dtype) {
                              : paged_kernel_type<64>(c.dtype, out_dtype, box);
 }
 
-// Workspace: the error word and one ticket per CTA, two partials per CTA for
-// other CTAs and one per warp for its own.
+// Workspace: the error word and one ticket per CTA, and two partials per CTA.
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t ticket_bytes(int ctas) { return align256((size_t)(kPagedTickets + ctas) * 4); }
 
-size_t part_bytes(const PagedKernel& k, int ctas) {
-    return align256((size_t)ctas * 2 * k.part_floats * 4);
-}
-
 size_t workspace_bytes_for(const PagedKernel& k, int ctas) {
-    return ticket_bytes(ctas) + part_bytes(k, ctas) +
-           align256((size_t)ctas * (k.threads / 32) * k.part_floats * 4);
+    return ticket_bytes(ctas) + align256((size_t)ctas * 2 * k.part_floats * 4);
 }
 
 alspec_status check_heads(const alspec_paged_cache* c, int batch, int n_q_heads) {
@@ -386,8 +380,6 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
     p.lse = lse;
     p.ctr = static_cast<unsigned*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(ctas));
-    p.heads = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(ctas) +
-                                       part_bytes(kern, ctas));
     p.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
     return launch(kern.fn, (unsigned)ctas, (unsigned)kern.threads, kern.smem, stream, p);
 }

@@ -370,7 +370,6 @@ struct PagedParams {
     float* lse;
     unsigned* ctr;  // error word and the tickets of the joins
     float* part;    // [CTA][2] partials for other CTAs
-    float* heads;   // [CTA][warp] partials of a warp's first run
     unsigned long long timeout_ns;
 };
 
@@ -401,7 +400,8 @@ struct PagedCfg {
         return r / BOX * (SEGS * SEG) + r % BOX * SEGB;
     }
     static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
-    static constexpr int kOffScale = NW * ST * STAGEB;
+    static constexpr int kOffHead = NW * ST * STAGEB;  // partials of the warps' first runs
+    static constexpr int kOffScale = kOffHead + NW * PART * 4;
     static constexpr int kOffMeta = kOffScale + (T == kPagesE4m3 ? NW * ST * 2 * kTile * 4 : 0);
     static constexpr int kOffBar = kOffMeta + NW * ST * 16;
     static constexpr int kOffPiece = kOffBar + NW * ST * 8;
@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::ST;
     int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * C::ST;
     float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * kTile;
-    float* deposit0 = p.heads + ((long long)blockIdx.x * C::NW + warp) * C::PART;
+    float* deposit0 = reinterpret_cast<float*>(smem + C::kOffHead) + warp * C::PART;
     const int units = p.hkv * p.blocks;
     // A warp's barriers are its own: no other warp has to see them.
     if (lane == 0) {
@@ -1180,8 +1180,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     // Join what spans warps: runs of pieces of one (sequence, unit).  Piece 2 i
     // is warp i's first run, piece 2 i + 1 its last; every lane holds one.
     auto partial = [&](int i) {
-        return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * C::ST * C::STAGEB)
-                       : p.heads + ((long long)blockIdx.x * C::NW + (i >> 1)) * C::PART;
+        return reinterpret_cast<const float*>(
+            smem + ((i & 1) ? (i >> 1) * (C::ST * C::STAGEB)
+                            : C::kOffHead + (i >> 1) * (C::PART * 4)));
     };
     static_assert(2 * C::NW <= 32, "a lane per piece");
     PagedPiece a{};
