@@ -116,9 +116,11 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     if (!x || !w || !y || !aligned16(x) || !aligned16(w)) return ALSPEC_ERR_INVALID_ARG;
 
     LinearParams p{};
-    // Batch rows per tile: equal shares of at most 256, in steps of 16 (the
-    // step of a 128-row tcgen05 shape).
-    p.row_tiles = (int)(((int64_t)rows + kLinMaxN - 1) / kLinMaxN);
+    // Batch rows per tile: equal shares of at most 256 (fp32 outputs: 128, for
+    // room in TMEM, see below), in steps of 16 (the step of a 128-row tcgen05
+    // shape).
+    const int most = out_dtype == ALSPEC_F32 ? kLinMaxN / 2 : kLinMaxN;
+    p.row_tiles = (int)(((int64_t)rows + most - 1) / most);
     p.nt = (int)((((int64_t)rows + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16);
     p.row_tiles = (rows - 1) / p.nt + 1;
     const int64_t tiles = ((int64_t)n + kLinM - 1) / kLinM * p.row_tiles;
@@ -141,8 +143,14 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     const int stage = (kLinM + p.nt) * 128 * p.group;
     const int fills = ((p.kblocks + p.split - 1) / p.split + p.group - 1) / p.group;
     p.stages = std::min({kLinMaxStages, ring / stage, std::max(2, fills)});
-    p.tmem_cols = 32;
-    while (p.tmem_cols < p.nt) p.tmem_cols *= 2;
+    // An MMA's sum may lose 2^-23 of its running value at every step: for fp32
+    // outputs the blocks go round several accumulators, as many as TMEM holds,
+    // up to eight (16 x 8192 x 8192: 4.4e-6 of the result off with one, 1.0e-6
+    // with four; bf16 outputs round at 4e-3).
+    p.sum_cols = 32;
+    while (p.sum_cols < p.nt) p.sum_cols *= 2;
+    p.sums = out_dtype == ALSPEC_F32 ? std::min(8, 512 / p.sum_cols) : 1;
+    p.tmem_cols = p.sum_cols * p.sums;
     const int smem =
         std::max({p.stages * stage + exchange, p.push ? 0 : p.nt * kLinM * 4, kLinMinSmem}) + 1024;
     alspec_status st = encode_matrix(&p.tw, &p.tw_end, w, k, n, k, kLinM, p.group);

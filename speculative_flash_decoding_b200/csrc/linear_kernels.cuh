@@ -49,6 +49,7 @@ struct LinearParams {
     int row_tiles, split, stages;
     int group;     // 64-column blocks a stage holds
     int tmem_cols;
+    int sums, sum_cols;  // accumulators that the blocks go round, columns of each
     int out_bf16, act;
     int push;      // parts of the sums go to the CTA that finishes their rows
     int slice;     // batch rows that a CTA finishes, at most
@@ -97,7 +98,7 @@ __device__ __forceinline__ void lin_commit(uint64_t* bar) {
                  : "memory");
 }
 
-// 16 accumulator columns of this thread's lane.
+// 16 accumulator columns of this thread's lane, from the first accumulator.
 __device__ __forceinline__ void lin_load16(uint32_t addr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
@@ -111,6 +112,18 @@ __device__ __forceinline__ void lin_load16(uint32_t addr, float (&v)[16]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same, all accumulators added: `used` of them, sum_cols columns apart.
+__device__ __forceinline__ void lin_sum16(const LinearParams& p, uint32_t addr, int used,
+                                          float (&v)[16]) {
+    lin_load16(addr, v);
+    for (int a = 1; a < used; ++a) {
+        float w[16];
+        lin_load16(addr + (uint32_t)(a * p.sum_cols), w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += w[i];
+    }
 }
 
 // The activation of N sums: one branch on its kind, not one per sum.  SiLU
@@ -335,6 +348,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
             // fp32 accumulator, bf16 operands, both K-major.
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                    ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(kLinM >> 4) << 24);
+            int sum = 0;
             for (int i = 0; i < fills; ++i) {
                 const int s = i % p.stages;
                 if (!lin_wait(full + s, (i / p.stages) & 1, abort, p)) {
@@ -353,7 +367,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
                     const uint64_t db = lin_desc(a + p.group * kLinM * 128 + g * p.nt * 128);
 #pragma unroll
                     for (int k = 0; k < kLinK / 16; ++k)  // 32 bytes of every row a step
-                        lin_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || g > 0 || k > 0);
+                        lin_mma(tmem + (uint32_t)(sum * p.sum_cols), da + 2 * k, db + 2 * k, idesc,
+                                k > 0 || i * p.group + g >= p.sums);
+                    if (++sum == p.sums) sum = 0;
                 }
                 lin_commit(empty + s);
             }
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
             smem_addr(exchange) + (uint32_t)(rank * p.slice * kLinM + fl) * 4;
         for (int c = 16 * (warp >> 2); c < rows; c += 32) {
             float v[16];
-            lin_load16(taddr + c, v);
+            lin_sum16(p, taddr + c, min(p.sums, kb1 - kb0), v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (c + i < rows) {
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         float* mine = reinterpret_cast<float*>(ring);
         for (int c = 16 * (warp >> 2); c < rows; c += 32) {
             float v[16];
-            lin_load16(taddr + c, v);
+            lin_sum16(p, taddr + c, min(p.sums, kb1 - kb0), v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) mine[(c + i) * kLinM + fl] = v[i];
         }

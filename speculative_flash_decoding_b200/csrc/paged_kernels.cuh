@@ -422,7 +422,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int len) {
     PagedSeq s;
     s.len = min(max(len, 0), p.cap);
     const int all = (s.len + kTile - 1) / kTile;
-    if (p.S + p.W == 0) {
+    if ((p.S | p.W) == 0) {
         s.a = s.n = all;
         s.f = 0;
     } else {
@@ -718,6 +718,10 @@ struct PagedWarp {
         const uint32_t ka[2] = {stage + k_off, (stage + k_off) ^ 64u};
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
+            // For fp32 outputs the sums run in two halves, those of the low
+            // parts of fp32 keys apart: an MMA's sum may lose 2^-23 of its
+            // running value at every step.
+            float odd[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
@@ -727,7 +731,8 @@ struct PagedWarp {
                         f[1], f[2], f[3]);
                 if constexpr (kB16) {
                     mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[0], f[1]);
-                    mma_bf16_16816(s[n], qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, f[2], f[3]);
+                    mma_bf16_16816(T == kPagesBf16Wide ? odd : s[n], qa[c / 2 + 1][0], 0u,
+                                   qa[c / 2 + 1][1], 0u, f[2], f[3]);
                 } else if constexpr (T == kPagesE4m3) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -743,10 +748,15 @@ struct PagedWarp {
                         uint32_t h0, l0, h1, l1;
                         split_tf32(__uint_as_float(f[2 * i]), h0, l0);
                         split_tf32(__uint_as_float(f[2 * i + 1]), h1, l1);
-                        mma_tf32_1688(s[n], qa[k][0], qb[k][0], qa[k][1], qb[k][1], h0, h1);
-                        mma_tf32_1688(s[n], qa[k][0], qb[k][0], qa[k][1], qb[k][1], l0, l1);
+                        mma_tf32_1688(i ? odd : s[n], qa[k][0], qb[k][0], qa[k][1], qb[k][1], h0,
+                                      h1);
+                        mma_tf32_1688(low, qa[k][0], qb[k][0], qa[k][1], qb[k][1], l0, l1);
                     }
                 }
+            }
+            if constexpr (T == kPagesF32 || T == kPagesBf16Wide) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[n][i] += odd[i] + low[i];
             }
         }
         // Lane (r, j) holds head r, tokens 8 n + 2 j and + 1.  x: scores, up
@@ -1113,7 +1123,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             }
             // Tokens of the set: bit t of the mask.
             const int t = at.w + lane;
-            const bool on = t < s.len && (p.S + p.W == 0 || t < p.S || t >= s.len - p.W);
+            const bool on = t < s.len && ((p.S | p.W) == 0 || t < p.S || t >= s.len - p.W);
             const unsigned mask = __ballot_sync(0xffffffffu, on);
             unsigned char* stage = ring + slot * C::STAGEB;
             if (mask != 0xffffffffu) {

@@ -249,6 +249,47 @@ def test_decode_scale_and_no_lse(cuda_device):
     check_attention(got, None, ref, lens, 64, "bf16", F32)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("scale", [-0.2, 1e-30])
+def test_decode_unusual_scales(cuda_device, dtype, scale):
+    """A negative scale, and one that makes every weight equal."""
+    lens = [65, 300]
+    c = make_cache(dtype, lens, 16, 2, 64, seed=2)
+    _, q, _, got, lse = _decode(c, lens, 6, 64, F32, scale=scale, dtype=dtype, n_sink=3, window=50)
+    ref = attention(q, c["k64"], c["v64"], lens, 3, 50, scale=scale)
+    check_attention(got, lse, ref, lens, 64, dtype, F32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_decode_values_that_are_not_finite(cuda_device, dtype):
+    """NaN among the attended keys or values reaches the heads that read them
+    and no others; behind the end of a sequence, or outside the sink set, it
+    reaches nobody."""
+    from speculative_flash_decoding_b200 import PagedDecoder
+    lens = [200, 150]
+    c = make_cache(dtype, lens, 16, 2, 64, seed=2)
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(0))
+    q = q.to(F32 if dtype == "f32" else BF16).cuda()
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    nan = 0x7F if dtype == "e4m3" else math.nan
+
+    def poke(name, b, h, t):
+        x = c[name].view(torch.uint8) if dtype == "e4m3" else c[name]
+        x[c["table"][b, t // 16].long(), h, t % 16, 5] = nan
+
+    poke("k", 0, 1, 100)
+    poke("v", 1, 0, 100)
+    sinks = PagedDecoder(_cache(c), 2, 4, n_sink=4, window=40)
+    out = sinks.decode(q, c["table"], seq, out=torch.empty(2, 4, 64, device="cuda"))
+    assert bool(out.isfinite().all())
+    out = PagedDecoder(_cache(c), 2, 4).decode(q, c["table"], seq,
+                                               out=torch.empty(2, 4, 64, device="cuda"))
+    bad = torch.zeros(2, 4, 64, dtype=torch.bool, device="cuda")
+    bad[0, 2:] = True           # a NaN score
+    bad[1, :2, 5] = True        # a NaN value
+    assert torch.equal(out.isnan(), bad)
+
+
 def test_decode_v_scales_over_a_wide_range(cuda_device):
     """V scales that differ by 2^80 between tokens: the running power of two
     keeps every weight in range."""
