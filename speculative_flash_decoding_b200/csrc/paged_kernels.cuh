@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 //   bf16 pages  Q is exact; P = hi + lo (16 bits), for fp32 outputs a third
 //               bf16 term in a second MMA (24 bits);
 //   e4m3 pages  codes widen exactly to f16; Q, scaled by a power of two per
-//               head, and P are f16 hi + lo (22 bits).  The K scale
+//               head, is f16 (its bf16 fit), P f16 hi + lo (22 bits).  The K scale
 //               multiplies a score, the V scale a probability, which is kept
 //               in f16's range by a running power of two (vexp);
 //   fp32 pages  tf32 with hi + lo of both operands (22 bits).
@@ -594,7 +594,7 @@ struct PagedWarp {
     static constexpr int KS = T == kPagesF32 ? D / 8 : D / 16;  // k steps of Q K
     static constexpr int NT = D / 8;                            // output n tiles
     static constexpr int CH = C::RB / 16;                       // 16-byte chunks of a row
-    static constexpr bool kSplitQ = !kB16;
+    static constexpr bool kSplitQ = T == kPagesF32;
 
     uint32_t qa[KS][2];                    // A rows 0-7
     uint32_t qb[kSplitQ ? KS : 1][2];      // A rows 8-15: what qa's type rounds away
@@ -668,8 +668,10 @@ struct PagedWarp {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const uint32_t x = w ? raw[k].y : raw[k].x;
-                    split_f16(__uint_as_float(x << 16) * inv,
-                              __uint_as_float(x & 0xffff0000u) * inv, qa[k][w], qb[k][w]);
+                    // (Elements below 2^-14 of the largest lose what is below
+                    // 2^-25 of it.)
+                    qa[k][w] = pack_f16(__uint_as_float(x << 16) * inv,
+                                        __uint_as_float(x & 0xffff0000u) * inv);
                 }
         } else {
             const float* q = static_cast<const float*>(p.q) + at;
@@ -738,8 +740,7 @@ struct PagedWarp {
                     for (int i = 0; i < 4; ++i) {
                         uint32_t b0, b1;
                         e4m3x4_to_f16x4(f[i], b0, b1);
-                        mma_f16_16816(s[n], qa[c + i][0], qb[c + i][0], qa[c + i][1], qb[c + i][1],
-                                      b0, b1);
+                        mma_f16_16816(s[n], qa[c + i][0], 0u, qa[c + i][1], 0u, b0, b1);
                     }
                 } else {
 #pragma unroll
