@@ -49,7 +49,7 @@ std::mutex g_clusters_mutex;
 bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
     int dev = 0;
     if (!ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return false;
-    if (smem_attr_once(reinterpret_cast<const void*>(linear_kernel), kLinSmem) != ALSPEC_OK)
+    if (smem_attr_once(reinterpret_cast<const void*>(linear_kernel<false>), kLinSmem) != ALSPEC_OK)
         return false;
     std::lock_guard<std::mutex> lock(g_clusters_mutex);
     int(&n)[kLinMaxSplit + 1] = g_clusters[dev];
@@ -65,7 +65,7 @@ bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (!ok(cudaOccupancyMaxActiveClusters(&n[c], linear_kernel, &cfg)) || n[c] < 1) {
+        if (!ok(cudaOccupancyMaxActiveClusters(&n[c], linear_kernel<false>, &cfg)) || n[c] < 1) {
             n[kLinMaxSplit] = 0;
             return false;
         }
@@ -80,13 +80,14 @@ bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
 // hold 74 pairs, but 45 clusters of 3, 33 of 4, 26 of 5, 15 of 8), and a
 // second wave costs more than idle SMs: 33 x 4096 x 6144 (48 tiles) takes 24
 // us with 3, 19.6 with 5 and 15 with 2.
-int choose_split(int64_t tiles, int kblocks) {
+// `ctas`: CTAs that work on a tile's block of K together.
+int choose_split(int64_t tiles, int kblocks, int ctas) {
     int n[kLinMaxSplit + 1];
     if (!resident_clusters(n)) return 0;
     int best = 1;
     int64_t least = INT64_MAX;
-    for (int c = 1; c <= kLinMaxSplit && c <= std::max(1, kblocks / 4); ++c) {
-        const int64_t waves = (tiles + n[c] - 1) / n[c];
+    for (int c = 1; c * ctas <= kLinMaxSplit && c <= std::max(1, kblocks / 4); ++c) {
+        const int64_t waves = (tiles + n[c * ctas] - 1) / n[c * ctas];
         const int64_t cost = waves * ((kblocks + c - 1) / c + (c > 1 ? 20 : 16));
         if (cost < least) least = cost, best = c;
     }
@@ -123,12 +124,20 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     p.row_tiles = (int)(((int64_t)rows + most - 1) / most);
     p.nt = (int)((((int64_t)rows + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16);
     p.row_tiles = (rows - 1) / p.nt + 1;
-    const int64_t tiles = ((int64_t)n + kLinM - 1) / kLinM * p.row_tiles;
+    // Large batches: pairs of CTAs, so that each brings half of x.  From 250
+    // rows on x is more bytes than W: 250 x 8192 x 8192 took 43.6 us without.
+    const bool pair = p.nt > kLinPair && n > kLinM;
+    if (pair) {
+        p.nt = (p.nt + 31) / 32 * 32;
+        p.row_tiles = (rows - 1) / p.nt + 1;
+    }
+    const int ctas = pair ? 2 : 1;
+    const int64_t tiles = ((int64_t)n + ctas * kLinM - 1) / (ctas * kLinM) * p.row_tiles;
     p.kblocks = (k - 1) / kLinK + 1;
     p.whole = k / kLinK;
-    p.split = choose_split(tiles, p.kblocks);
+    p.split = choose_split(tiles, p.kblocks, ctas);
     if (p.split == 0) return ALSPEC_ERR_CUDA;
-    if (tiles * p.split > 0x7fffffff || n > 0x7fffffff - kLinM) return ALSPEC_ERR_UNSUPPORTED;
+    if (tiles * p.split * ctas > 0x7fffffff || n > 0x7fffffff - kLinM) return ALSPEC_ERR_UNSUPPORTED;
     // Blocks of a stage: four (512 consecutive bytes of a row of W) where the
     // ring holds two such stages, else two.  DRAM wants neighbouring columns
     // asked for together: one block a stage, a ring of 200 KB, took 35.1 us
@@ -139,8 +148,9 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     p.slice = (rows_tile + p.split - 1) / p.split;
     const int exchange = p.push ? p.split * p.slice * kLinM * 4 : 0;
     const int ring = kLinSmem - 1024 - exchange;
-    p.group = (kLinM + p.nt) * 128 * 8 <= ring ? 4 : 2;
-    const int stage = (kLinM + p.nt) * 128 * p.group;
+    const int block = (kLinM + p.nt / ctas) * 128;
+    p.group = block * 8 <= ring ? 4 : 2;
+    const int stage = block * p.group;
     const int fills = ((p.kblocks + p.split - 1) / p.split + p.group - 1) / p.group;
     p.stages = std::min({kLinMaxStages, ring / stage, std::max(2, fills)});
     // An MMA's sum may lose 2^-23 of its running value at every step: for fp32
@@ -155,8 +165,8 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
         std::max({p.stages * stage + exchange, p.push ? 0 : p.nt * kLinM * 4, kLinMinSmem}) + 1024;
     alspec_status st = encode_matrix(&p.tw, &p.tw_end, w, k, n, k, kLinM, p.group);
     if (st != ALSPEC_OK) return st;
-    if ((st = encode_matrix(&p.tx, &p.tx_end, x, k, rows, x_stride ? x_stride : k, p.nt,
-                            p.group)) != ALSPEC_OK)
+    if ((st = encode_matrix(&p.tx, &p.tx_end, x, k, rows, x_stride ? x_stride : k,
+                            p.nt / ctas, p.group)) != ALSPEC_OK)
         return st;
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.residual = residual;
@@ -170,19 +180,19 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
             !(reinterpret_cast<uintptr_t>(residual) & quad);
     p.err = err;
     p.timeout_ns = 2000000000ull;
-    const void* fn = reinterpret_cast<const void*>(linear_kernel);
-    if ((st = smem_attr_once(fn, kLinSmem)) != ALSPEC_OK) return st;
+    void (*const fn)(LinearParams) = pair ? linear_kernel<true> : linear_kernel<false>;
+    if ((st = smem_attr_once(reinterpret_cast<const void*>(fn), kLinSmem)) != ALSPEC_OK) return st;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * p.split));
+    cfg.gridDim = dim3((unsigned)(tiles * p.split * ctas));
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2] = {programmatic_launch()};
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.x = p.split * ctas;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return ok(cudaLaunchKernelEx(&cfg, linear_kernel, p)) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
+    return ok(cudaLaunchKernelEx(&cfg, fn, p)) ? ALSPEC_OK : ALSPEC_ERR_CUDA;
 }

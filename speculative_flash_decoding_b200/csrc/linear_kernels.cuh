@@ -30,6 +30,7 @@ constexpr int kLinMaxN = 256;     // batch rows per tile
 constexpr int kLinMaxStages = 12;
 constexpr int kLinSmem = 224 * 1024;  // dynamic shared memory, at most
 constexpr int kLinMaxSplit = 8;   // CTAs of a cluster
+constexpr int kLinPair = 128;     // batch rows of a tile up to which a CTA works alone
 constexpr int kLinPush = 48;      // batch rows of a small batch's tile, at most
 constexpr int kLinAhead = 8;      // blocks asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM
@@ -82,20 +83,70 @@ __device__ __forceinline__ uint64_t lin_desc(uint32_t addr) {
            (2ull << 61);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void lin_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
 }
 
-__device__ __forceinline__ void lin_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_addr(bar))
-                 : "memory");
+// Arrive on `bar` (PAIR: of both CTAs, `first` the pair's lower rank in the
+// cluster) once the MMAs so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void lin_commit(uint64_t* bar, int first) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+            ".multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+            "h"((uint16_t)(3 << first))
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_addr(bar))
+            : "memory");
+}
+
+// TMEM columns, for one warp of the CTA (PAIR: of each CTA of the pair).
+template <bool PAIR>
+__device__ __forceinline__ void lin_tmem_alloc(uint32_t* at, uint32_t columns) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(at)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(at)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void lin_tmem_free(uint32_t tmem, uint32_t columns) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(columns)
+                     : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(columns)
+                     : "memory");
 }
 
 // 16 accumulator columns of this thread's lane, from the first accumulator.
@@ -165,12 +216,12 @@ __device__ __forceinline__ void lin_put4(__nv_bfloat16* p, const float* v) {
 }
 
 // The epilogue of batch rows [c0, c1) of a tile.  Their sums lie in shared
-// memory, either one part in each of the cluster's CTAs, [row][feature], or
-// (PUSH) all parts here, [CTA][row - c0][feature].  A warp takes a row at a
+// memory, either one part in each of the cluster's CTAs (of its half, where
+// CTAS is 2), [row][feature], or (PUSH) all parts here, [CTA][row - c0][feature].  A warp takes a row at a
 // time, a lane four features; everything a round of R rows needs is asked for
 // before it is used (rounds of four rows: 44.1 us for 250 x 8192 x 8192).
-template <typename O, bool PUSH, int R>
-__device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int rank,
+template <typename O, bool PUSH, int CTAS, int R>
+__device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int place,
                                              int c0, int c1, int r0, int n0) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kWarps = kLinThreads / 32;
@@ -207,13 +258,13 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
         for (int s = 0; s < p.split; ++s) {
             // This CTA's own part without the way through the cluster.
             float4 part[R];
-            if (PUSH || s == rank) {
+            if (PUSH || s == place / CTAS) {
                 const uint32_t from = here + (uint32_t)(PUSH ? s * p.slice * kLinM * 4 : 0);
 #pragma unroll
                 for (int u = 0; u < R; ++u)
                     if (c + u * kWarps < c1) part[u] = lds_v4(from + u * kWarps * kLinM * 4);
             } else {
-                const uint32_t from = dsmem_addr(here, s);
+                const uint32_t from = dsmem_addr(here, (uint32_t)(s * CTAS + place % CTAS));
 #pragma unroll
                 for (int u = 0; u < R; ++u)
                     if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
@@ -248,6 +299,11 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
     }
 }
 
+// PAIR: two CTAs of a cluster (ranks 2 i and 2 i + 1) work as one on 256
+// features: each brings its own 128 rows of W and half of the rows of x, the
+// first issues MMAs of twice the M that read both CTAs' shared memory, and
+// each keeps the sums of its own features.
+template <bool PAIR>
 __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     const __grid_constant__ LinearParams p) {
     extern __shared__ unsigned char lin_raw[];
@@ -259,13 +315,18 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     unsigned char* ring = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(lin_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)blockIdx.x % p.split, tile = (int)blockIdx.x / p.split;
+    constexpr int kCtas = PAIR ? 2 : 1;  // that work on one tile's block of K
+    const int place = (int)blockIdx.x % (kCtas * p.split);  // in the cluster
+    const int tile = (int)blockIdx.x / (kCtas * p.split);
+    const int rank = place / kCtas, half = place % kCtas;
+    const int first = place - half;
     // Row tiles of one feature tile are neighbours: its W comes from L2 for
     // all but the first.
-    const int n0 = tile / p.row_tiles * kLinM, r0 = tile % p.row_tiles * p.nt;
+    const int n0 = (tile / p.row_tiles * kCtas + half) * kLinM, r0 = tile % p.row_tiles * p.nt;
+    const int xr = p.nt / kCtas;  // rows of x that this CTA brings
     const int kb0 = (int)((long long)rank * p.kblocks / p.split);
     const int kb1 = (int)((long long)(rank + 1) * p.kblocks / p.split);
-    const int stage_bytes = (kLinM + p.nt) * 128 * p.group;
+    const int stage_bytes = (kLinM + xr) * 128 * p.group;
     const int fills = (kb1 - kb0 + p.group - 1) / p.group;
     const int rows = min(p.nt, p.rows - r0);
     const int c0 = rank * rows / p.split, c1 = (rank + 1) * rows / p.split;  // this CTA finishes
@@ -290,14 +351,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         prefetch_tmap(&p.tx_end);
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(&tmem_base)),
-                     "r"((uint32_t)p.tmem_cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        lin_tmem_alloc<PAIR>(&tmem_base, (uint32_t)p.tmem_cols);
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     }
-    __syncthreads();
+    // (A pair's CTAs signal each other's barriers.)
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_base;
     // Launched while the kernel ahead on the stream may still run: nothing is
@@ -305,7 +366,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     // one be launched.
     // (W's first stages are asked for in L2 meanwhile, which is coherent
     // whoever writes them: 16 x 8192 x 8192 back to back 25.9 -> 24.5 us.)
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && lane == 0 && n0 < p.n) {
         for (int i = 0; i < kLinAhead / p.group; ++i) {
             const int kb = kb0 + i * p.group;
             if (kb + p.group <= min(kb1, p.whole)) tma_prefetch_3d(&p.tw, 0, n0, kb);
@@ -327,27 +388,43 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
                 const int kb = kb0 + i * p.group;
                 unsigned char* w = ring + s * stage_bytes;
                 unsigned char* x = w + p.group * kLinM * 128;
-                if (kb + p.group <= min(kb1, p.whole)) {
-                    mbar_arrive_expect_tx(full + s, (uint32_t)stage_bytes);
+                const int blocks = min(p.group, kb1 - kb), rx = r0 + half * xr;
+                // The barrier of the CTA that issues the MMAs takes the bytes
+                // of both.
+                if (half == 0)
+                    mbar_arrive_expect_tx(full + s,
+                                          (uint32_t)(kCtas * blocks * (kLinM + xr) * 128));
+                if constexpr (PAIR) {
+                    const uint32_t bar = dsmem_addr(smem_addr(full + s), (uint32_t)first);
+                    if (kb + p.group <= min(kb1, p.whole)) {
+                        tma_load_3d_pair(w, &p.tw, 0, n0, kb, bar, policy);
+                        tma_load_3d_pair(x, &p.tx, 0, rx, kb, bar, keep);
+                    } else {
+                        for (int g = 0; g < blocks; ++g) {
+                            tma_load_2d_pair(w + g * kLinM * 128, &p.tw_end, (kb + g) * kLinK, n0,
+                                             bar, policy);
+                            tma_load_2d_pair(x + g * xr * 128, &p.tx_end, (kb + g) * kLinK, rx,
+                                             bar, keep);
+                        }
+                    }
+                } else if (kb + p.group <= min(kb1, p.whole)) {
                     tma_load_3d(w, &p.tw, 0, n0, kb, full + s, policy);
-                    tma_load_3d(x, &p.tx, 0, r0, kb, full + s, keep);
+                    tma_load_3d(x, &p.tx, 0, rx, kb, full + s, keep);
                 } else {  // the last blocks of this CTA, one at a time
-                    const int blocks = min(p.group, kb1 - kb);
-                    mbar_arrive_expect_tx(full + s, (uint32_t)(blocks * (kLinM + p.nt) * 128));
                     for (int g = 0; g < blocks; ++g) {
                         tma_load_2d(w + g * kLinM * 128, &p.tw_end, (kb + g) * kLinK, n0, full + s,
                                     policy);
-                        tma_load_2d(x + g * p.nt * 128, &p.tx_end, (kb + g) * kLinK, r0, full + s,
+                        tma_load_2d(x + g * xr * 128, &p.tx_end, (kb + g) * kLinK, rx, full + s,
                                     keep);
                     }
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && half == 0) {
             // fp32 accumulator, bf16 operands, both K-major.
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
-                                   ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(kLinM >> 4) << 24);
+                                   ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(kCtas * kLinM >> 4) << 24);
             int sum = 0;
             for (int i = 0; i < fills; ++i) {
                 const int s = i % p.stages;
@@ -364,16 +441,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
                 const int blocks = min(p.group, kb1 - kb0 - i * p.group);
                 for (int g = 0; g < blocks; ++g) {
                     const uint64_t da = lin_desc(a + g * kLinM * 128);
-                    const uint64_t db = lin_desc(a + p.group * kLinM * 128 + g * p.nt * 128);
+                    const uint64_t db = lin_desc(a + p.group * kLinM * 128 + g * xr * 128);
 #pragma unroll
                     for (int k = 0; k < kLinK / 16; ++k)  // 32 bytes of every row a step
-                        lin_mma(tmem + (uint32_t)(sum * p.sum_cols), da + 2 * k, db + 2 * k, idesc,
-                                k > 0 || i * p.group + g >= p.sums);
+                        lin_mma<PAIR>(tmem + (uint32_t)(sum * p.sum_cols), da + 2 * k, db + 2 * k,
+                                      idesc, k > 0 || i * p.group + g >= p.sums);
                     if (++sum == p.sums) sum = 0;
                 }
-                lin_commit(empty + s);
+                lin_commit<PAIR>(empty + s, first);
             }
-            lin_commit(&done);
+            lin_commit<PAIR>(&done, first);
         }
     } else if (p.residual) {
         // Meanwhile the residual is asked for in L2.
@@ -395,7 +472,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     // alternate groups of 16 columns.
     const int fl = (warp & 3) * 32 + lane;  // feature within the tile
     const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    if (p.push) {
+    if (!PAIR && p.push) {
         // Small batches: a part goes straight to the CTA that finishes the
         // row, into a buffer beside the ring, and one cluster barrier later
         // every CTA is on its own.  (Reading the others' parts needs a second
@@ -421,13 +498,15 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
             __syncthreads();
         if (good) {
             if (p.out_bf16)
-                lin_epilogue<__nv_bfloat16, true, 2>(p, smem_addr(exchange), rank, c0, c1, r0, n0);
+                lin_epilogue<__nv_bfloat16, true, 1, 2>(p, smem_addr(exchange), place, c0, c1, r0,
+                                                        n0);
             else
-                lin_epilogue<float, true, 2>(p, smem_addr(exchange), rank, c0, c1, r0, n0);
+                lin_epilogue<float, true, 1, 2>(p, smem_addr(exchange), place, c0, c1, r0, n0);
         }
     } else {
         // Large batches: this CTA's parts, [batch row][feature], go where the
-        // ring was, and every CTA reads those of the rows it finishes.
+        // ring was, and every CTA reads those of the rows it finishes (a
+        // pair's CTAs have features of their own: the ranks of one half).
         float* mine = reinterpret_cast<float*>(ring);
         for (int c = 16 * (warp >> 2); c < rows; c += 32) {
             float v[16];
@@ -441,18 +520,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
             __syncthreads();
         if (good) {
             if (p.out_bf16)
-                lin_epilogue<__nv_bfloat16, false, 8>(p, smem_addr(mine), rank, c0, c1, r0, n0);
+                lin_epilogue<__nv_bfloat16, false, kCtas, 8>(p, smem_addr(mine), place, c0, c1,
+                                                             r0, n0);
             else
-                lin_epilogue<float, false, 8>(p, smem_addr(mine), rank, c0, c1, r0, n0);
+                lin_epilogue<float, false, kCtas, 8>(p, smem_addr(mine), place, c0, c1, r0, n0);
         }
-        if (p.split > 1) cluster_sync();
+        if (PAIR || p.split > 1) cluster_sync();
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"((uint32_t)p.tmem_cols)
-                     : "memory");
+    if (warp == 2) lin_tmem_free<PAIR>(tmem, (uint32_t)p.tmem_cols);
 }
 
 }  // namespace alspec

@@ -218,6 +218,29 @@ __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* tmap, in
         : "memory");
 }
 
+// tma_load_2d and tma_load_3d of a CTA pair (tcgen05 cta_group::2): the bytes
+// count on an mbarrier of either CTA of the pair, `bar` its address in the
+// cluster.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst_smem, const void* tmap, int x, int y,
+                                                 uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(
+            smem_addr(dst_smem)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst_smem, const void* tmap, int x, int y,
+                                                 int z, uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(
+            smem_addr(dst_smem)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
+        : "memory");
+}
+
 // The same box brought into L2 only.
 __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(

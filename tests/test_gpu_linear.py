@@ -61,6 +61,12 @@ def _check(y, x, w, b, r, act):
     (257, 300, 96, "none", F32, True, False, 0),
     (700, 129, 1032, "silu", BF16, True, True, 8),
     (2, 20000, 136, "none", F32, True, False, 0),
+    # Pairs of CTAs: batches of more than 128 rows with bf16 outputs.
+    (250, 256, 512, "none", BF16, False, False, 0),
+    (129, 257, 64, "gelu", BF16, True, True, 0),
+    (200, 1000, 4096, "silu", BF16, True, True, 8),
+    (250, 8192, 1024, "none", BF16, True, False, 0),
+    (1000, 140, 72, "relu", BF16, True, True, 0),
 ])
 def test_linear(cuda_device, rows, n, k, act, out, bias, residual, pad):
     from speculative_flash_decoding_b200 import Linear
