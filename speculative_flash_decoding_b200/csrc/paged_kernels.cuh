@@ -252,15 +252,17 @@ struct GatherParams {
     const int* table;
     const int* lens;
     void* out[2];
-    int batch, max_pages, max_len, blocks_per_head;
+    int max_pages, max_len, blocks_per_seq;
     unsigned* err;
 };
 
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 64;  // tokens per CTA
 
-// One CTA reads back 64 tokens of one (sequence, KV head), K and V; D / 8
-// lanes hold a row.  Bound by bytes.
+// A CTA reads back 64 tokens of one sequence, K and V, of every gridDim.y'th
+// KV head; D / 8 lanes hold a row.  Bound by bytes.  (One CTA for all heads,
+// where that leaves CTAs enough: 64 tokens behind the end of a sequence cost
+// one CTA that finds nothing to do, not one a head.)
 template <int SRC, int DST, int D>
 __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
     const __grid_constant__ GatherParams p) {
@@ -268,49 +270,56 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
     constexpr int RPI = kGatherThreads / LPR;  // rows per iteration
     pdl_wait_prerequisite();
     pdl_launch_dependents();
-    const unsigned bh = blockIdx.x / p.blocks_per_head;
-    const int t0 = (int)(blockIdx.x % p.blocks_per_head) * kGatherRows;
-    const int b = bh / p.lay.hkv, h = bh % p.lay.hkv;
-    int len = __ldg(p.lens + b);
-    const long long cap = min((long long)p.max_len, (long long)p.max_pages * p.lay.page_size);
-    if (len < 0 || len > cap) {
-        if (p.err && threadIdx.x == 0 && t0 == 0 && h == 0) atomicOr(p.err, kErrSeqLen);
-        len = len < 0 ? 0 : (int)cap;
-    }
     const int col = (int)(threadIdx.x % LPR) * 8;
+    const int cap = (int)min((long long)p.max_len, (long long)p.max_pages * p.lay.page_size);
+    const int b = (int)(blockIdx.x / (unsigned)p.blocks_per_seq);
+    const int t0 = (int)(blockIdx.x - (unsigned)b * (unsigned)p.blocks_per_seq) * kGatherRows;
+    int len = __ldg(p.lens + b);
+    if (len < 0 || len > cap) {
+        if (p.err && threadIdx.x == 0 && t0 == 0 && blockIdx.y == 0) atomicOr(p.err, kErrSeqLen);
+        len = len < 0 ? 0 : cap;
+    }
+    if (t0 >= len) return;
+    for (int h = blockIdx.y; h < p.lay.hkv; h += gridDim.y) {
+        const long long bh = (long long)b * p.lay.hkv + h;
 #pragma unroll
-    for (int i = 0; i < kGatherRows / RPI; ++i) {
-        const int t = t0 + i * RPI + (int)threadIdx.x / LPR;
-        if (t >= len) continue;
-        const int page = __ldg(p.table + (long long)b * p.max_pages + t / p.lay.page_size);
-        if (page < 0 || page >= p.lay.n_pages) {
-            if (p.err && col == 0) atomicOr(p.err, kErrPage);
-            continue;
-        }
-        const int slot = t % p.lay.page_size;
-        const long long src = p.lay.row(page, h, slot) + col;
-        const long long dst = ((long long)bh * p.max_len + t) * D + col;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            float x[8];
-            if constexpr (SRC == kE4m3) {
-                const uint2 c = __ldg(reinterpret_cast<const uint2*>(
-                    static_cast<const uint8_t*>(p.pages[w]) + src));
-                const float s = __ldg(p.scales[w] + p.lay.scale(page, h, slot));
-                const uint32_t r[2] = {c.x, c.y};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t f = e4m3x2_to_f16x2((uint16_t)(r[j / 2] >> (16 * (j % 2))));
-                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                    x[2 * j] = v.x * s;
-                    x[2 * j + 1] = v.y * s;
-                }
-            } else {
-                Raw8<SRC> raw;
-                raw.load(p.pages[w], src);
-                raw.unpack(x);
+        for (int i = 0; i < kGatherRows / RPI; ++i) {
+            const int t = t0 + i * RPI + (int)threadIdx.x / LPR;
+            if (t >= len) continue;
+            const int page = __ldg(p.table + (long long)b * p.max_pages + t / p.lay.page_size);
+            if (page < 0 || page >= p.lay.n_pages) {
+                if (p.err && col == 0) atomicOr(p.err, kErrPage);
+                continue;
             }
-            store8<DST>(p.out[w], dst, x);
+            const int slot = t % p.lay.page_size;
+            const long long src = p.lay.row(page, h, slot) + col;
+            const long long dst = (bh * p.max_len + t) * D + col;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                float x[8];
+                if constexpr (SRC == kE4m3) {
+                    const uint2 c = __ldg(reinterpret_cast<const uint2*>(
+                        static_cast<const uint8_t*>(p.pages[w]) + src));
+                    const float s = __ldg(p.scales[w] + p.lay.scale(page, h, slot));
+                    const uint32_t r[2] = {c.x, c.y};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t f[2];
+                        e4m3x4_to_f16x4(r[j], f[0], f[1]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[k]));
+                            x[4 * j + 2 * k] = v.x * s;
+                            x[4 * j + 2 * k + 1] = v.y * s;
+                        }
+                    }
+                } else {
+                    Raw8<SRC> raw;
+                    raw.load(p.pages[w], src);
+                    raw.unpack(x);
+                }
+                store8<DST>(p.out[w], dst, x);
+            }
         }
     }
 }
