@@ -348,9 +348,10 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 //               multiplies a score, the V scale a probability, which is kept
 //               in f16's range by a running power of two (vexp);
 //   fp32 pages  tf32 with hi + lo of both operands (22 bits).
-// Bound by HBM bytes while a scheduler has two or more warps: with one warp
-// each (4 warps a CTA) a warp's own latency bounded it (an instruction every
-// 5 cycles; 128K tokens of bf16 112 us instead of the figure below).
+// Bound by HBM bytes over bf16 pages (128K tokens of 8 KV heads: 84 us, 6.4
+// TB/s), by instructions over e4m3 pages (8 x 16K-64K tokens: 148 us, 5.3 TB/s;
+// a tile of 8 KB takes 128 conversions and 64 MMAs), by the reads before the
+// first tile and the joins after the last where the sequences are short.
 
 constexpr int kTile = 32;       // tokens
 constexpr int kHeadRows = 8;    // query heads per work unit
@@ -725,49 +726,71 @@ struct PagedWarp {
     __device__ __forceinline__ void tile(uint32_t stage, unsigned mask, const float* ks,
                                          const float* vs, int lane) {
         const int j = lane & 3;
+        // Scores of four groups of 8 tokens; over fp32 pages the groups' MMAs
+        // in turn (4 x 20000 tokens of 128 elements 146 -> 140 us).
         float s[4][4];
         const uint32_t ka[2] = {stage + k_off, (stage + k_off) ^ 64u};
+        // For fp32 outputs the sums run in two halves, those of the low parts
+        // of fp32 keys apart: an MMA's sum may lose 2^-23 of its running value
+        // at every step.
+        constexpr bool kHalves = T == kPagesF32 || T == kPagesBf16Wide;
+        float odd[kHalves ? 4 : 1][4], low[T == kPagesF32 ? 4 : 1][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            // For fp32 outputs the sums run in two halves, those of the low
-            // parts of fp32 keys apart: an MMA's sum may lose 2^-23 of its
-            // running value at every step.
-            float odd[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                s[n][i] = 0.f;
+                if constexpr (kHalves) odd[n][i] = 0.f;
+                if constexpr (T == kPagesF32) low[n][i] = 0.f;
+            }
 #pragma unroll
-            for (int c = 0; c < CH; c += 4) {
-                uint32_t f[4];
-                ldsm_x4(ka[(c >> 2) & 1] + (uint32_t)(C::row(8 * n) + (c >> 3) * C::SEG), f[0],
-                        f[1], f[2], f[3]);
-                if constexpr (kB16) {
-                    mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[0], f[1]);
-                    mma_bf16_16816(T == kPagesBf16Wide ? odd : s[n], qa[c / 2 + 1][0], 0u,
-                                   qa[c / 2 + 1][1], 0u, f[2], f[3]);
-                } else if constexpr (T == kPagesE4m3) {
+        for (int c = 0; c < CH; c += 4) {
+            uint32_t f[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                ldsm_x4(ka[(c >> 2) & 1] + (uint32_t)(C::row(8 * n) + (c >> 3) * C::SEG), f[n][0],
+                        f[n][1], f[n][2], f[n][3]);
+            if constexpr (kB16) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[n][0], f[n][1]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    mma_bf16_16816(kHalves ? odd[kHalves ? n : 0] : s[n], qa[c / 2 + 1][0], 0u,
+                                   qa[c / 2 + 1][1], 0u, f[n][2], f[n][3]);
+            } else if constexpr (T == kPagesE4m3) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t b0, b1;
-                        e4m3x4_to_f16x4(f[i], b0, b1);
+                        e4m3x4_to_f16x4(f[n][i], b0, b1);
                         mma_f16_16816(s[n], qa[c + i][0], 0u, qa[c + i][1], 0u, b0, b1);
                     }
-                } else {
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
                         const int k = c / 2 + i;
                         uint32_t h0, l0, h1, l1;
-                        split_tf32(__uint_as_float(f[2 * i]), h0, l0);
-                        split_tf32(__uint_as_float(f[2 * i + 1]), h1, l1);
-                        mma_tf32_1688(i ? odd : s[n], qa[k][0], qb[k][0], qa[k][1], qb[k][1], h0,
-                                      h1);
-                        mma_tf32_1688(low, qa[k][0], qb[k][0], qa[k][1], qb[k][1], l0, l1);
+                        split_tf32(__uint_as_float(f[n][2 * i]), h0, l0);
+                        split_tf32(__uint_as_float(f[n][2 * i + 1]), h1, l1);
+                        mma_tf32_1688(i ? odd[kHalves ? n : 0] : s[n], qa[k][0], qb[kSplitQ ? k : 0][0],
+                                      qa[k][1], qb[kSplitQ ? k : 0][1], h0, h1);
+                        mma_tf32_1688(low[T == kPagesF32 ? n : 0], qa[k][0], qb[kSplitQ ? k : 0][0],
+                                      qa[k][1], qb[kSplitQ ? k : 0][1], l0, l1);
                     }
-                }
             }
-            if constexpr (T == kPagesF32 || T == kPagesBf16Wide) {
+        }
+        if constexpr (kHalves) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] += odd[i] + low[i];
-            }
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[n][i] += odd[n][i];
+                    if constexpr (T == kPagesF32) s[n][i] += low[n][i];
+                }
         }
         // Lane (r, j) holds head r, tokens 8 n + 2 j and + 1.  x: scores, up
         // to the factor `f` that makes them logarithms to base 2.
