@@ -854,7 +854,10 @@ struct PagedWarp {
             }
         m = m_new;
         l = l * alpha + sum;
-        if (__any_sync(0xffffffffu, rescale != 1.f)) {
+        // For fp32 outputs a tile's products are summed apart and then added,
+        // because the MMAs' sums lose towards zero (one chain over all of a
+        // warp's tiles: 1.8e-5 of the result at 2 x 16 x 55854 fp32 tokens).
+        if (!kHalves && __any_sync(0xffffffffu, rescale != 1.f)) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -866,69 +869,109 @@ struct PagedWarp {
             // Rows 2 j and 2 j + 1 of a k step: the second is 128 bytes on,
             // its chunks exchanged by the swizzle.
             const uint32_t v1 = (v0 + 128u) ^ 16u;
+            uint32_t hi[4][2], lo[4][2];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {  // tokens 8 n ..: k step n
-                uint32_t h0, l0, h1, l1;
-                split_tf32(x[n][0], h0, l0);
-                split_tf32(x[n][1], h1, l1);
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const uint32_t add = (uint32_t)(C::row(8 * n) + (i >> 2) * C::SEG);
-                    const uint32_t flip = (uint32_t)((2 * i & 7) << 4);
-                    uint32_t a0, a1, b0, b1;
-                    split_tf32(lds((v0 ^ flip) + add), a0, a1);
-                    split_tf32(lds((v1 ^ flip) + add), b0, b1);
-                    mma_tf32_1688(acc[i], h0, l0, h1, l1, a0, b0);
-                    mma_tf32_1688(acc[i], h0, l0, h1, l1, a1, b1);
-                }
+                for (int i = 0; i < 2; ++i) split_tf32(x[n][i], hi[n][i], lo[n][i]);
+#pragma unroll
+            for (int i0 = 0; i0 < NT; i0 += 2) {
+                float sum[2][4] = {};
+#pragma unroll
+                for (int n = 0; n < 4; ++n)  // tokens 8 n ..: k step n
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int i = i0 + w;
+                        const uint32_t add = (uint32_t)(C::row(8 * n) + (i >> 2) * C::SEG);
+                        const uint32_t flip = (uint32_t)((2 * i & 7) << 4);
+                        uint32_t a0, a1, b0, b1;
+                        split_tf32(lds((v0 ^ flip) + add), a0, a1);
+                        split_tf32(lds((v1 ^ flip) + add), b0, b1);
+                        mma_tf32_1688(sum[w], hi[n][0], lo[n][0], hi[n][1], lo[n][1], a0, b0);
+                        mma_tf32_1688(sum[w], hi[n][0], lo[n][0], hi[n][1], lo[n][1], a1, b1);
+                    }
+                add_sums(i0, rescale, sum);
             }
         } else {
+            uint32_t a[2][4], third[2][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {  // tokens 16 k ..
-                uint32_t a[4], c0 = 0, c1 = 0;
                 if constexpr (T == kPagesE4m3) {
-                    split_f16(x[2 * k][0], x[2 * k][1], a[0], a[1]);
-                    split_f16(x[2 * k + 1][0], x[2 * k + 1][1], a[2], a[3]);
+                    split_f16(x[2 * k][0], x[2 * k][1], a[k][0], a[k][1]);
+                    split_f16(x[2 * k + 1][0], x[2 * k + 1][1], a[k][2], a[k][3]);
                 } else {
-                    a[0] = take_bf16(x[2 * k][0], x[2 * k][1]);
-                    a[1] = take_bf16(x[2 * k][0], x[2 * k][1]);
-                    a[2] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
-                    a[3] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
+                    a[k][0] = take_bf16(x[2 * k][0], x[2 * k][1]);
+                    a[k][1] = take_bf16(x[2 * k][0], x[2 * k][1]);
+                    a[k][2] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
+                    a[k][3] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
                     if constexpr (T == kPagesBf16Wide) {
-                        c0 = take_bf16(x[2 * k][0], x[2 * k][1]);
-                        c1 = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
-                    }
-                }
-                // Matrices of one ldmatrix: tokens 0-7 and 8-15 of the step,
-                // chunks c and c + 1.
-#pragma unroll
-                for (int c = 0; c < CH; c += 2) {
-                    uint32_t f4[4];
-                    ldsm_x4_t((v0 ^ (uint32_t)((c & 7) << 4)) +
-                                  (uint32_t)(C::row(16 * k) + (c >> 3) * C::SEG),
-                              f4[0], f4[1], f4[2], f4[3]);
-                    if constexpr (T == kPagesE4m3) {
-                        // A code pair of one token per half word: split into
-                        // the even and the odd column's tokens.
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            uint32_t even0, odd0, even1, odd1;
-                            e4m3x4_to_f16x4(__byte_perm(f4[2 * w], 0u, 0x3120), even0, odd0);
-                            e4m3x4_to_f16x4(__byte_perm(f4[2 * w + 1], 0u, 0x3120), even1, odd1);
-                            mma_f16_16816(acc[2 * (c + w)], a[0], a[1], a[2], a[3], even0, even1);
-                            mma_f16_16816(acc[2 * (c + w) + 1], a[0], a[1], a[2], a[3], odd0, odd1);
-                        }
-                    } else {
-                        mma_bf16_16816(acc[c], a[0], a[1], a[2], a[3], f4[0], f4[1]);
-                        mma_bf16_16816(acc[c + 1], a[0], a[1], a[2], a[3], f4[2], f4[3]);
-                        if constexpr (T == kPagesBf16Wide) {
-                            mma_bf16_16816(acc[c], c0, 0u, c1, 0u, f4[0], f4[1]);
-                            mma_bf16_16816(acc[c + 1], c0, 0u, c1, 0u, f4[2], f4[3]);
-                        }
+                        third[k][0] = take_bf16(x[2 * k][0], x[2 * k][1]);
+                        third[k][1] = take_bf16(x[2 * k + 1][0], x[2 * k + 1][1]);
                     }
                 }
             }
+            // Matrices of one ldmatrix: tokens 0-7 and 8-15 of a step, chunks
+            // c and c + 1.
+            auto load = [&](int k, int c, uint32_t (&f)[4]) {
+                ldsm_x4_t((v0 ^ (uint32_t)((c & 7) << 4)) +
+                              (uint32_t)(C::row(16 * k) + (c >> 3) * C::SEG),
+                          f[0], f[1], f[2], f[3]);
+            };
+            if constexpr (T == kPagesBf16Wide) {
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                    float sum[2][4] = {};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t f[4];
+                        load(k, c, f);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            mma_bf16_16816(sum[w], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * w],
+                                           f[2 * w + 1]);
+                            mma_bf16_16816(sum[w], third[k][0], 0u, third[k][1], 0u, f[2 * w],
+                                           f[2 * w + 1]);
+                        }
+                    }
+                    add_sums(c, rescale, sum);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int c = 0; c < CH; c += 2) {
+                        uint32_t f[4];
+                        load(k, c, f);
+                        if constexpr (T == kPagesE4m3) {
+                            // A code pair of one token per half word: split
+                            // into the even and the odd column's tokens.
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                uint32_t even0, odd0, even1, odd1;
+                                e4m3x4_to_f16x4(__byte_perm(f[2 * w], 0u, 0x3120), even0, odd0);
+                                e4m3x4_to_f16x4(__byte_perm(f[2 * w + 1], 0u, 0x3120), even1,
+                                                odd1);
+                                mma_f16_16816(acc[2 * (c + w)], a[k][0], a[k][1], a[k][2], a[k][3],
+                                              even0, even1);
+                                mma_f16_16816(acc[2 * (c + w) + 1], a[k][0], a[k][1], a[k][2],
+                                              a[k][3], odd0, odd1);
+                            }
+                        } else {
+                            mma_bf16_16816(acc[c], a[k][0], a[k][1], a[k][2], a[k][3], f[0], f[1]);
+                            mma_bf16_16816(acc[c + 1], a[k][0], a[k][1], a[k][2], a[k][3], f[2],
+                                           f[3]);
+                        }
+                    }
+            }
         }
+    }
+
+    // A tile's sums of output tiles i and i + 1 onto the running ones.
+    __device__ __forceinline__ void add_sums(int i, float rescale, const float (&sum)[2][4]) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i + w][k] = fmaf(acc[i + w][k], rescale, sum[w][k]);
     }
 
     // Calls f(column, value, value of column + 1) for this lane's elements of
