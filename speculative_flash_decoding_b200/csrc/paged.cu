@@ -155,7 +155,9 @@ PagedKernel paged_kernel_box(int box) {
 template <int D>
 PagedKernel paged_kernel_type(int dtype, int out_dtype, int box) {
     return dtype == ALSPEC_F32        ? paged_kernel_box<kPagesF32, D>(box)
-           : dtype == ALSPEC_E4M3     ? paged_kernel_box<kPagesE4m3, D>(box)
+           : dtype == ALSPEC_E4M3
+               ? (out_dtype == ALSPEC_BF16 ? paged_kernel_box<kPagesE4m3, D>(box)
+                                           : paged_kernel_box<kPagesE4m3Wide, D>(box))
            : out_dtype == ALSPEC_BF16 ? paged_kernel_box<kPagesBf16, D>(box)
                                       : paged_kernel_box<kPagesBf16Wide, D>(box);
 }

@@ -356,9 +356,18 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 constexpr int kTile = 32;       // tokens
 constexpr int kHeadRows = 8;    // query heads per work unit
 
-// Page types of the decode kernel: bf16 pages with fp32 outputs carry a
-// third term of P.
-enum : int { kPagesF32 = 0, kPagesBf16 = 1, kPagesE4m3 = 2, kPagesBf16Wide = 3 };
+// Page types of the decode kernel.  Wide: for fp32 outputs (bf16 pages: P with
+// a third term; both: a tile's products summed apart).
+enum : int {
+    kPagesF32 = 0,
+    kPagesBf16 = 1,
+    kPagesE4m3 = 2,
+    kPagesBf16Wide = 3,
+    kPagesE4m3Wide = 4
+};
+__host__ __device__ constexpr bool pages_e4m3(int t) {
+    return t == kPagesE4m3 || t == kPagesE4m3Wide;
+}
 
 struct PagedParams {
     CUtensorMap tk, tv;  // 5-D: (element, slot, 128-byte segment, KV head, page)
@@ -389,7 +398,7 @@ constexpr int kPagedTickets = kCtrFixed;  // one ticket per CTA follows
 // (rows of more than 128 bytes: a box holds its rows segment by segment).
 template <int T, int D, int BOX>
 struct PagedCfg {
-    static constexpr int ES = T == kPagesF32 ? 4 : T == kPagesE4m3 ? 1 : 2;
+    static constexpr int ES = T == kPagesF32 ? 4 : pages_e4m3(T) ? 1 : 2;
     static constexpr int RB = D * ES;                     // bytes of a row
     static constexpr int SEGB = RB < 128 ? RB : 128;      // bytes of a box row
     static constexpr int SEGS = RB / SEGB;                // boxes side by side
@@ -412,7 +421,7 @@ struct PagedCfg {
     static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
     static constexpr int kOffHead = NW * ST * STAGEB;  // partials of the warps' first runs
     static constexpr int kOffScale = kOffHead + NW * PART * 4;
-    static constexpr int kOffMeta = kOffScale + (T == kPagesE4m3 ? NW * ST * 2 * kTile * 4 : 0);
+    static constexpr int kOffMeta = kOffScale + (pages_e4m3(T) ? NW * ST * 2 * kTile * 4 : 0);
     static constexpr int kOffBar = kOffMeta + NW * ST * 16;
     static constexpr int kOffPiece = kOffBar + NW * ST * 8;
     static constexpr int kOffMisc = kOffPiece + 2 * NW * 32;
@@ -605,6 +614,7 @@ struct PagedWarp {
     static constexpr int NT = D / 8;                            // output n tiles
     static constexpr int CH = C::RB / 16;                       // 16-byte chunks of a row
     static constexpr bool kSplitQ = T == kPagesF32;
+    static constexpr bool kApart = T == kPagesF32 || T == kPagesBf16Wide || T == kPagesE4m3Wide;
 
     uint32_t qa[KS][2];                    // A rows 0-7
     uint32_t qb[kSplitQ ? KS : 1][2];      // A rows 8-15: what qa's type rounds away
@@ -650,7 +660,7 @@ struct PagedWarp {
                 qa[k][0] = live ? __ldg(q + 8 * k + j) ^ flip : 0u;
                 qa[k][1] = live ? __ldg(q + 8 * k + j + 4) ^ flip : 0u;
             }
-        } else if constexpr (T == kPagesE4m3) {
+        } else if constexpr (pages_e4m3(T)) {
             // Lane j of a quad holds elements 16 k + 4 j .. + 3 of k step k:
             // the order in which the codes of K come out of ldmatrix.
             const uint2* q = reinterpret_cast<const uint2*>(
@@ -758,7 +768,7 @@ struct PagedWarp {
                 for (int n = 0; n < 4; ++n)
                     mma_bf16_16816(kHalves ? odd[kHalves ? n : 0] : s[n], qa[c / 2 + 1][0], 0u,
                                    qa[c / 2 + 1][1], 0u, f[n][2], f[n][3]);
-            } else if constexpr (T == kPagesE4m3) {
+            } else if constexpr (pages_e4m3(T)) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -800,7 +810,7 @@ struct PagedWarp {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 x[n][i] = kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i];
-            if constexpr (T == kPagesE4m3) {
+            if constexpr (pages_e4m3(T)) {
                 const float2 kk = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * j);
                 const float2 vv = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * j);
                 x[n][0] *= kk.x * rowscale;
@@ -809,7 +819,7 @@ struct PagedWarp {
                 vsc[n][1] = vv.y;
             }
         }
-        if constexpr (T == kPagesE4m3) f = 1.f;
+        if constexpr (pages_e4m3(T)) f = 1.f;
         if (mask != 0xffffffffu) {
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -829,7 +839,7 @@ struct PagedWarp {
         const float base = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = m == m_new ? 1.f : fast_exp2(m - base);
         float rescale = alpha, vinv = 1.f;
-        if constexpr (T == kPagesE4m3) {
+        if constexpr (pages_e4m3(T)) {
 #pragma unroll
             for (int n = 0; n < 4; ++n) vmax = fmaxf(vmax, fmaxf(fabsf(vsc[n][0]), fabsf(vsc[n][1])));
             vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
@@ -850,14 +860,14 @@ struct PagedWarp {
             for (int i = 0; i < 2; ++i) {
                 x[n][i] = fast_exp2(fmaf(x[n][i], f, -base));
                 sum += x[n][i];
-                if constexpr (T == kPagesE4m3) x[n][i] *= vsc[n][i] * vinv;
+                if constexpr (pages_e4m3(T)) x[n][i] *= vsc[n][i] * vinv;
             }
         m = m_new;
         l = l * alpha + sum;
         // For fp32 outputs a tile's products are summed apart and then added,
         // because the MMAs' sums lose towards zero (one chain over all of a
         // warp's tiles: 1.8e-5 of the result at 2 x 16 x 55854 fp32 tokens).
-        if (!kHalves && __any_sync(0xffffffffu, rescale != 1.f)) {
+        if (!kApart && __any_sync(0xffffffffu, rescale != 1.f)) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -896,7 +906,7 @@ struct PagedWarp {
             uint32_t a[2][4], third[2][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {  // tokens 16 k ..
-                if constexpr (T == kPagesE4m3) {
+                if constexpr (pages_e4m3(T)) {
                     split_f16(x[2 * k][0], x[2 * k][1], a[k][0], a[k][1]);
                     split_f16(x[2 * k + 1][0], x[2 * k + 1][1], a[k][2], a[k][3]);
                 } else {
@@ -935,6 +945,27 @@ struct PagedWarp {
                     }
                     add_sums(c, rescale, sum);
                 }
+            } else if constexpr (T == kPagesE4m3Wide) {
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                    float sum[2][2][4] = {};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t f[4];
+                        load(k, c, f);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            uint32_t b0[2], b1[2];
+                            codes_of(f[2 * w], f[2 * w + 1], b0, b1);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                mma_f16_16816(sum[w][e], a[k][0], a[k][1], a[k][2], a[k][3], b0[e],
+                                              b1[e]);
+                        }
+                    }
+                    add_sums(2 * c, rescale, sum[0]);
+                    add_sums(2 * c + 2, rescale, sum[1]);
+                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -942,19 +973,15 @@ struct PagedWarp {
                     for (int c = 0; c < CH; c += 2) {
                         uint32_t f[4];
                         load(k, c, f);
-                        if constexpr (T == kPagesE4m3) {
-                            // A code pair of one token per half word: split
-                            // into the even and the odd column's tokens.
+                        if constexpr (pages_e4m3(T)) {
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
-                                uint32_t even0, odd0, even1, odd1;
-                                e4m3x4_to_f16x4(__byte_perm(f[2 * w], 0u, 0x3120), even0, odd0);
-                                e4m3x4_to_f16x4(__byte_perm(f[2 * w + 1], 0u, 0x3120), even1,
-                                                odd1);
-                                mma_f16_16816(acc[2 * (c + w)], a[k][0], a[k][1], a[k][2], a[k][3],
-                                              even0, even1);
-                                mma_f16_16816(acc[2 * (c + w) + 1], a[k][0], a[k][1], a[k][2],
-                                              a[k][3], odd0, odd1);
+                                uint32_t b0[2], b1[2];
+                                codes_of(f[2 * w], f[2 * w + 1], b0, b1);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    mma_f16_16816(acc[2 * (c + w) + e], a[k][0], a[k][1], a[k][2],
+                                                  a[k][3], b0[e], b1[e]);
                             }
                         } else {
                             mma_bf16_16816(acc[c], a[k][0], a[k][1], a[k][2], a[k][3], f[0], f[1]);
@@ -964,6 +991,15 @@ struct PagedWarp {
                     }
             }
         }
+    }
+
+    // V codes of tokens 0-7 and 8-15 as ldmatrix leaves them (a pair of columns
+    // of one token per half word) to the operands of the even and the odd
+    // column.
+    __device__ __forceinline__ static void codes_of(uint32_t low, uint32_t high, uint32_t (&b0)[2],
+                                                    uint32_t (&b1)[2]) {
+        e4m3x4_to_f16x4(__byte_perm(low, 0u, 0x3120), b0[0], b0[1]);
+        e4m3x4_to_f16x4(__byte_perm(high, 0u, 0x3120), b1[0], b1[1]);
     }
 
     // A tile's sums of output tiles i and i + 1 onto the running ones.
@@ -983,7 +1019,7 @@ struct PagedWarp {
         for (int i = 0; i < NT; i += 2)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if constexpr (T == kPagesE4m3) {
+                if constexpr (pages_e4m3(T)) {
                     // Tiles i and i + 1 hold the even and odd columns of 16.
                     f(8 * i + 4 * j + 2 * k, (acc[i][k] + acc[i][k + 2]) * vexp,
                       (acc[i + 1][k] + acc[i + 1][k + 2]) * vexp);
@@ -1047,7 +1083,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     const int units = p.hkv * p.blocks;
     // A warp's barriers are its own: no other warp has to see them.
     if (lane == 0) {
-        for (int s = 0; s < C::ST; ++s) mbar_init(full + s, T == kPagesE4m3 ? 33 : 1);
+        for (int s = 0; s < C::ST; ++s) mbar_init(full + s, pages_e4m3(T) ? 33 : 1);
         fence_barrier_init();
         prefetch_tmap(&p.tk);
         prefetch_tmap(&p.tv);
@@ -1124,7 +1160,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                     tma_load_5d(dst + C::TILEB, &p.tv, in, h, pg, full + slot, pol);
                 }
             }
-            if constexpr (T == kPagesE4m3) {
+            if constexpr (pages_e4m3(T)) {
                 // Lane = token: its scales, and its arrival once they landed.
                 const int pg = __shfl_sync(0xffffffffu, page, from);
                 const int in = __shfl_sync(0xffffffffu, in_page, from) + rem;

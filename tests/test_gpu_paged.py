@@ -469,14 +469,13 @@ def test_long_sums_keep_fp32(cuda_device, dtype, out):
     products lose at most eight steps of 2^-23 (towards zero, so the whole
     shrinks by 2^-20 at most), tiles are added rounding to nearest (2^-24
     each, without a direction), and scores and exponentials are within 2^-21
-    on the average.  e4m3 pages add a tile's two steps to one running sum:
-    2^-23 a step, at random where the output's sign is, 2^-18 allowed."""
+    on the average."""
     lens = [30000] * 8
     c = make_cache(dtype, lens, 64, 2, 64, seed=21)
     _, q, _, got, _ = _decode(c, lens, 4, 64, out, dtype=dtype)
     ref = attention(q, c["k64"], c["v64"], lens)[0]
     rel = float((got.double().cpu() - ref).norm() / ref.norm())
-    assert rel <= 2.0 ** (-18 if dtype == "e4m3" else -19), rel
+    assert rel <= 2.0 ** -19, rel
 
 
 def test_shared_pages(cuda_device):
