@@ -563,8 +563,9 @@ size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, i
  *   timeout_ms  bound on any in-kernel wait; 0 = 2000
  * Rows behind L_b in the last page may hold anything, NaN included.  Sums and
  * softmax statistics are fp32; results do not depend on timing (no float
- * atomics).  Any group size n_q_heads / n_kv_heads; batch <= 65535, and batch *
- * max_pages * page_size below about 2^36 (ALSPEC_ERR_UNSUPPORTED).
+ * atomics).  Any group size n_q_heads / n_kv_heads; batch <= 65535, and
+ * max_pages * page_size times the batch, or times n_q_heads, below 2^34
+ * (ALSPEC_ERR_UNSUPPORTED from there or a little later on).
  * Asynchronous on `stream`, one launch, no allocation; safe to capture.
  */
 alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q, int64_t q_stride,

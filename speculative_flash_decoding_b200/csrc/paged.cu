@@ -134,22 +134,27 @@ using PagedFn = void (*)(PagedParams);
 struct PagedKernel {
     PagedFn fn;
     int threads, smem, part_floats;
+    int tile, box;  // tokens of a tile, rows of a TMA box
 };
 
 template <int T, int D, int BOX>
-PagedKernel paged_kernel() {
+PagedKernel paged_kernel(int box) {
     using C = PagedCfg<T, D, BOX>;
-    return PagedKernel{paged_decode_kernel<T, D, BOX>, C::kThreads, C::kSmemBytes, C::PART};
+    return PagedKernel{paged_decode_kernel<T, D, BOX>, C::kThreads, C::kSmemBytes, C::PART, C::TT,
+                       box};
 }
 
-// Rows of up to 128 bytes lie the same way whatever the box.
+// `box`: the largest power of two that divides a page; a box takes that, up
+// to a tile.  Rows of up to 128 bytes lie the same way whatever the box.
 template <int T, int D>
 PagedKernel paged_kernel_box(int box) {
-    if constexpr (PagedCfg<T, D, kTile>::SEGS > 1) {
-        if (box == 8) return paged_kernel<T, D, 8>();
-        if (box == 16) return paged_kernel<T, D, 16>();
+    using C = PagedCfg<T, D, 8>;
+    box = std::min(box, C::TT);
+    if constexpr (C::SEGS > 1) {
+        if (box == 8) return paged_kernel<T, D, 8>(box);
+        if (C::TT > 16 && box == 16) return paged_kernel<T, D, 16>(box);
     }
-    return paged_kernel<T, D, kTile>();
+    return paged_kernel<T, D, C::TT>(box);
 }
 
 template <int D>
@@ -162,12 +167,8 @@ PagedKernel paged_kernel_type(int dtype, int out_dtype, int box) {
                                       : paged_kernel_box<kPagesBf16Wide, D>(box);
 }
 
-// Rows of a TMA box: the largest power of two up to a tile that divides a
-// page (8, 16 or 32).
-int box_rows(int page_size) { return std::min(kTile, page_size & -page_size); }
-
 PagedKernel paged_kernel_for(const alspec_paged_cache& c, int out_dtype) {
-    const int box = box_rows(c.page_size);
+    const int box = c.page_size & -c.page_size;
     return c.head_dim == 128 ? paged_kernel_type<128>(c.dtype, out_dtype, box)
                              : paged_kernel_type<64>(c.dtype, out_dtype, box);
 }
@@ -338,6 +339,14 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
         return ALSPEC_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return ALSPEC_ERR_WORKSPACE;
     const PagedKernel kern = paged_kernel_for(*cache, out_dtype);
+    const int group = n_q_heads / cache->n_kv_heads;
+    const int blocks = (group + kHeadRows - 1) / kHeadRows;
+    const int cap = table_tokens(max_pages, cache->page_size);
+    // The running sums of a batch's tiles are 32-bit, and so is a tile's place
+    // among those of a sequence's units.
+    if (std::max<int64_t>(batch, (int64_t)cache->n_kv_heads * blocks) * (cap / kern.tile + 2) >=
+        (1ll << 31))
+        return ALSPEC_ERR_UNSUPPORTED;
     const int ctas = sm_count_for_plan();
     if (workspace_bytes < workspace_bytes_for(kern, ctas)) return ALSPEC_ERR_WORKSPACE;
     if ((st = smem_attr_once(reinterpret_cast<const void*>(kern.fn), kern.smem)) != ALSPEC_OK)
@@ -345,7 +354,7 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
 
     PagedParams p{};
     const PageLayout l = layout_of(*cache);
-    p.box = box_rows(cache->page_size);
+    p.box = kern.box;
     if ((st = encode_pages(&p.tk, cache->k_pages, *cache, l, p.box)) != ALSPEC_OK) return st;
     if ((st = encode_pages(&p.tv, cache->v_pages, *cache, l, p.box)) != ALSPEC_OK) return st;
     p.q = q;
@@ -357,14 +366,12 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
     p.batch = batch;
     p.hq = n_q_heads;
     p.hkv = cache->n_kv_heads;
-    p.group = n_q_heads / cache->n_kv_heads;
-    p.blocks = (p.group + kHeadRows - 1) / kHeadRows;
+    p.group = group;
+    p.blocks = blocks;
     p.max_pages = max_pages;
     p.page_size = cache->page_size;
     p.n_pages = cache->n_pages;
-    p.cap = table_tokens(max_pages, cache->page_size);
-    // The running sums of a batch's tiles are 32-bit.
-    if ((int64_t)batch * (p.cap / kTile + 2) >= (1ll << 31)) return ALSPEC_ERR_UNSUPPORTED;
+    p.cap = cap;
     // No sequence is longer than cap, so neither term says more.
     p.S = std::min(n_sink, p.cap);
     p.W = std::min(window, p.cap);

@@ -353,7 +353,6 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 // a tile of 8 KB takes 128 conversions and 64 MMAs), by the reads before the
 // first tile and the joins after the last where the sequences are short.
 
-constexpr int kTile = 32;       // tokens
 constexpr int kHeadRows = 8;    // query heads per work unit
 
 // Page types of the decode kernel.  Wide: for fp32 outputs (bf16 pages: P with
@@ -403,15 +402,18 @@ struct PagedCfg {
     static constexpr int SEGB = RB < 128 ? RB : 128;      // bytes of a box row
     static constexpr int SEGS = RB / SEGB;                // boxes side by side
     static constexpr int SEG = BOX * SEGB;                // one segment of a box
-    static constexpr int TILEB = kTile * RB;              // K or V of a tile
+    // Tokens of a tile; rows of 512 bytes 16, so that six warps have room
+    // instead of three (4 x 20000 tokens of 128 fp32 elements 159 -> 128 us).
+    static constexpr int TT = RB > 256 ? 16 : 32;
+    static constexpr int TILEB = TT * RB;                 // K or V of a tile
+    static constexpr unsigned kAll = 0xffffffffu >> (32 - TT);  // a full tile's mask
     static constexpr int STAGEB = 2 * TILEB;
     // Warps, and two stages each.  128 KB on their way keep HBM busy; 192 KB
     // made the SMs unequal (128K tokens of bf16: some CTAs done after 60 us,
     // some after 85; 87.6 us a call against 84.2, 30000 x 8 of 64 bf16
     // elements 87.2 against 81.0), 96 KB took 90.4 us.  fp32 pages cost more
-    // instructions a byte: as many warps as fit.
-    static constexpr int NW = STAGEB >= 32768 ? 3 : STAGEB >= 16384 ? (T == kPagesF32 ? 6 : 4)
-                              : STAGEB >= 8192 ? 8 : 16;
+    // instructions a byte: six warps, as many as fit.
+    static constexpr int NW = STAGEB >= 16384 ? (T == kPagesF32 ? 6 : 4) : STAGEB >= 8192 ? 8 : 16;
     static constexpr int ST = 2;
     static constexpr int kThreads = NW * 32;
     // Offset of a row (a multiple of 8, or its row within 8 added later).
@@ -421,33 +423,35 @@ struct PagedCfg {
     static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
     static constexpr int kOffHead = NW * ST * STAGEB;  // partials of the warps' first runs
     static constexpr int kOffScale = kOffHead + NW * PART * 4;
-    static constexpr int kOffMeta = kOffScale + (pages_e4m3(T) ? NW * ST * 2 * kTile * 4 : 0);
+    static constexpr int kOffMeta = kOffScale + (pages_e4m3(T) ? NW * ST * 2 * TT * 4 : 0);
     static constexpr int kOffBar = kOffMeta + NW * ST * 16;
     static constexpr int kOffPiece = kOffBar + NW * ST * 8;
     static constexpr int kOffMisc = kOffPiece + 2 * NW * 32;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
+    static_assert(BOX <= TT, "a box of one tile");
     static_assert(ST >= 2 && PART * 4 <= ST * STAGEB, "ring");
     static_assert(kOffMeta % 16 == 0 && kOffPiece % 16 == 0, "alignment");
 };
 
-// Tiles of one sequence: tile i covers tokens [32 i, 32 i + 32) for i < a and
-// [32 (i + f - a), ...) from there on; every tile holds a token of the set.
+// Tiles of one sequence: tile i covers tokens [TT i, TT i + TT) for i < a and
+// [TT (i + f - a), ...) from there on; every tile holds a token of the set.
 struct PagedSeq {
     int len, n, a, f;
 };
 
+template <int TT>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int len) {
     PagedSeq s;
     s.len = min(max(len, 0), p.cap);
-    const int all = (s.len + kTile - 1) / kTile;
+    const int all = (s.len + TT - 1) / TT;
     if ((p.S | p.W) == 0) {
         s.a = s.n = all;
         s.f = 0;
     } else {
-        s.a = (min(p.S, s.len) + kTile - 1) / kTile;
+        s.a = (min(p.S, s.len) + TT - 1) / TT;
         const int w0 = max(0, s.len - p.W);
-        s.f = max(s.a, w0 / kTile);
+        s.f = max(s.a, w0 / TT);
         s.n = s.a + (w0 < s.len ? all - s.f : 0);
     }
     return s;
@@ -478,6 +482,7 @@ __device__ __forceinline__ int warp_inclusive(int x) {
     return x;
 }
 
+template <int TT>
 __device__ __forceinline__ PagedBatch paged_batch(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
     PagedBatch s;
@@ -487,7 +492,7 @@ __device__ __forceinline__ PagedBatch paged_batch(const PagedParams& p) {
 #pragma unroll 4
     for (int b = lane * s.chunk; b < min(p.batch, (lane + 1) * s.chunk); ++b) {
         s.len = __ldg(p.lens + b);
-        s.n += paged_seq(p, s.len).n;
+        s.n += paged_seq<TT>(p, s.len).n;
     }
     s.incl = warp_inclusive(s.n);
     s.total = (long long)__shfl_sync(0xffffffffu, s.incl, 31) * s.units;
@@ -496,6 +501,7 @@ __device__ __forceinline__ PagedBatch paged_batch(const PagedParams& p) {
 
 // The place of tile x (0 <= x < total) in the numbering (sequence, unit,
 // tile); called by a whole warp.
+template <int TT>
 __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const PagedBatch& t,
                                                long long x) {
     const int lane = threadIdx.x & 31;
@@ -505,13 +511,13 @@ __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const Paged
     long long before = __shfl_sync(0xffffffffu, t.incl, w) - n;
     r.b = w;
     if (t.chunk == 1) {
-        r.s = paged_seq(p, __shfl_sync(0xffffffffu, t.len, w));
+        r.s = paged_seq<TT>(p, __shfl_sync(0xffffffffu, t.len, w));
     } else {
         // The same among the sequences of that lane.
         for (int b0 = w * t.chunk;; b0 += 32) {
             const int b = b0 + lane;
             const bool in = b < min(p.batch, (w + 1) * t.chunk);
-            const int m = in ? paged_seq(p, __ldg(p.lens + b)).n : 0;
+            const int m = in ? paged_seq<TT>(p, __ldg(p.lens + b)).n : 0;
             const int incl = warp_inclusive(m);
             const unsigned past =
                 __ballot_sync(0xffffffffu, (before + incl) * t.units > x);
@@ -524,7 +530,7 @@ __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const Paged
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
-        r.s = paged_seq(p, __ldg(p.lens + r.b));
+        r.s = paged_seq<TT>(p, __ldg(p.lens + r.b));
     }
     const unsigned off = (unsigned)(x - before * t.units);
     r.u = (int)(off / (unsigned)n);
@@ -613,6 +619,8 @@ struct PagedWarp {
     static constexpr int KS = T == kPagesF32 ? D / 8 : D / 16;  // k steps of Q K
     static constexpr int NT = D / 8;                            // output n tiles
     static constexpr int CH = C::RB / 16;                       // 16-byte chunks of a row
+    static constexpr int NG = C::TT / 8;                        // groups of 8 tokens
+    static_assert(NG == 4 || T == kPagesF32, "tiles of 16-bit MMAs");
     static constexpr bool kSplitQ = T == kPagesF32;
     static constexpr bool kApart = T == kPagesF32 || T == kPagesBf16Wide || T == kPagesE4m3Wide;
 
@@ -736,17 +744,17 @@ struct PagedWarp {
     __device__ __forceinline__ void tile(uint32_t stage, unsigned mask, const float* ks,
                                          const float* vs, int lane) {
         const int j = lane & 3;
-        // Scores of four groups of 8 tokens; over fp32 pages the groups' MMAs
-        // in turn (4 x 20000 tokens of 128 elements 146 -> 140 us).
-        float s[4][4];
+        // Scores of groups of 8 tokens; over fp32 pages the groups' MMAs in
+        // turn.
+        float s[NG][4];
         const uint32_t ka[2] = {stage + k_off, (stage + k_off) ^ 64u};
         // For fp32 outputs the sums run in two halves, those of the low parts
         // of fp32 keys apart: an MMA's sum may lose 2^-23 of its running value
         // at every step.
         constexpr bool kHalves = T == kPagesF32 || T == kPagesBf16Wide;
-        float odd[kHalves ? 4 : 1][4], low[T == kPagesF32 ? 4 : 1][4];
+        float odd[kHalves ? NG : 1][4], low[T == kPagesF32 ? NG : 1][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[n][i] = 0.f;
@@ -755,22 +763,22 @@ struct PagedWarp {
             }
 #pragma unroll
         for (int c = 0; c < CH; c += 4) {
-            uint32_t f[4][4];
+            uint32_t f[NG][4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NG; ++n)
                 ldsm_x4(ka[(c >> 2) & 1] + (uint32_t)(C::row(8 * n) + (c >> 3) * C::SEG), f[n][0],
                         f[n][1], f[n][2], f[n][3]);
             if constexpr (kB16) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < NG; ++n)
                     mma_bf16_16816(s[n], qa[c / 2][0], 0u, qa[c / 2][1], 0u, f[n][0], f[n][1]);
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < NG; ++n)
                     mma_bf16_16816(kHalves ? odd[kHalves ? n : 0] : s[n], qa[c / 2 + 1][0], 0u,
                                    qa[c / 2 + 1][1], 0u, f[n][2], f[n][3]);
             } else if constexpr (pages_e4m3(T)) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t b0, b1;
@@ -781,7 +789,7 @@ struct PagedWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < NG; ++n) {
                         const int k = c / 2 + i;
                         uint32_t h0, l0, h1, l1;
                         split_tf32(__uint_as_float(f[n][2 * i]), h0, l0);
@@ -795,7 +803,7 @@ struct PagedWarp {
         }
         if constexpr (kHalves) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     s[n][i] += odd[n][i];
@@ -804,9 +812,9 @@ struct PagedWarp {
         }
         // Lane (r, j) holds head r, tokens 8 n + 2 j and + 1.  x: scores, up
         // to the factor `f` that makes them logarithms to base 2.
-        float x[4][2], vsc[4][2], vmax = 0.f, f = rowscale;
+        float x[NG][2], vsc[NG][2], vmax = 0.f, f = rowscale;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < NG; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 x[n][i] = kSplitQ ? s[n][i] + s[n][i + 2] : s[n][i];
@@ -820,16 +828,16 @@ struct PagedWarp {
             }
         }
         if constexpr (pages_e4m3(T)) f = 1.f;
-        if (mask != 0xffffffffu) {
+        if (mask != C::kAll) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (!((mask >> (8 * n + 2 * j + i)) & 1u)) x[n][i] = -INFINITY, vsc[n][i] = 0.f;
         }
         float mx = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) mx = fmaxf(mx, fmaxf(x[n][0], x[n][1]));
+        for (int n = 0; n < NG; ++n) mx = fmaxf(mx, fmaxf(x[n][0], x[n][1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * f;
         // The reference of the exponentials follows the maximum only when it
@@ -841,7 +849,7 @@ struct PagedWarp {
         float rescale = alpha, vinv = 1.f;
         if constexpr (pages_e4m3(T)) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) vmax = fmaxf(vmax, fmaxf(fabsf(vsc[n][0]), fabsf(vsc[n][1])));
+            for (int n = 0; n < NG; ++n) vmax = fmaxf(vmax, fmaxf(fabsf(vsc[n][0]), fabsf(vsc[n][1])));
             vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
             vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
             // The power of two at or below the largest V scale so far; 1 /
@@ -855,7 +863,7 @@ struct PagedWarp {
         }
         float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 x[n][i] = fast_exp2(fmaf(x[n][i], f, -base));
@@ -879,16 +887,16 @@ struct PagedWarp {
             // Rows 2 j and 2 j + 1 of a k step: the second is 128 bytes on,
             // its chunks exchanged by the swizzle.
             const uint32_t v1 = (v0 + 128u) ^ 16u;
-            uint32_t hi[4][2], lo[4][2];
+            uint32_t hi[NG][2], lo[NG][2];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) split_tf32(x[n][i], hi[n][i], lo[n][i]);
 #pragma unroll
             for (int i0 = 0; i0 < NT; i0 += 2) {
                 float sum[2][4] = {};
 #pragma unroll
-                for (int n = 0; n < 4; ++n)  // tokens 8 n ..: k step n
+                for (int n = 0; n < NG; ++n)  // tokens 8 n ..: k step n
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         const int i = i0 + w;
@@ -1078,7 +1086,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     unsigned char* ring = smem + warp * C::ST * C::STAGEB;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::ST;
     int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * C::ST;
-    float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * kTile;
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * C::TT;
     float* deposit0 = reinterpret_cast<float*>(smem + C::kOffHead) + warp * C::PART;
     const int units = p.hkv * p.blocks;
     // A warp's barriers are its own: no other warp has to see them.
@@ -1095,7 +1103,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     pdl_wait_prerequisite();
     pdl_launch_dependents();
 
-    const PagedBatch batch = paged_batch(p);
+    const PagedBatch batch = paged_batch<C::TT>(p);
     const long long total = batch.total;
     const long long workers = min((long long)gridDim.x * C::NW, total);
     const long long w = (long long)blockIdx.x * C::NW + warp;
@@ -1118,20 +1126,20 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     };
 
     if (tiles > 0) {
-        PagedPos pos = paged_find(p, batch, x0);
+        PagedPos pos = paged_find<C::TT>(p, batch, x0);
         const PagedPos start = pos;
         const uint64_t pol = p.blocks == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
         // A tile comes in boxes of `box` rows, K's and V's; lane i keeps the
         // page of box i.
         const int box = C::SEGS > 1 ? BOX : p.box;
-        const int down = kTile / box;
+        const int down = C::TT / box;
         const int sub = lane & (down - 1);
         const int from = lane / box, rem = lane % box;
         int page = 0;    // of this lane's box in the next tile to be issued
         int in_page = 0;
         int t0 = 0;      // that tile's first token
         auto fetch_page = [&]() {
-            t0 = (pos.i < pos.s.a ? pos.i : pos.i + pos.s.f - pos.s.a) * kTile;
+            t0 = (pos.i < pos.s.a ? pos.i : pos.i + pos.s.f - pos.s.a) * C::TT;
             const int t = t0 + sub * box;
             const int entry = (int)(__umulhi((unsigned)t, p.page_mul) >> p.page_shift);
             in_page = t - entry * p.page_size;
@@ -1141,7 +1149,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             const int left = pos.s.len - t0;  // tokens from here on
             const int h = p.blocks == 1 ? pos.u : pos.u / p.blocks;
             unsigned char* stage = ring + slot * C::STAGEB;
-            const int boxes = left >= kTile ? down : (left + box - 1) / box;
+            const int boxes = left >= C::TT ? down : (left + box - 1) / box;
             if (sub < boxes && (unsigned)page >= (unsigned)p.n_pages) {
                 atomicOr(p.ctr + kCtrError, kErrPage);
                 page = 0;
@@ -1166,8 +1174,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                 const int in = __shfl_sync(0xffffffffu, in_page, from) + rem;
                 if (lane < left) {
                     const long long at = ((long long)pg * p.hkv + h) * p.page_size + in;
-                    cp_async_4(scales + slot * 2 * kTile + lane, p.ks + at);
-                    cp_async_4(scales + slot * 2 * kTile + kTile + lane, p.vs + at);
+                    cp_async_4(scales + slot * 2 * C::TT + lane, p.ks + at);
+                    cp_async_4(scales + slot * 2 * C::TT + C::TT + lane, p.vs + at);
                 }
                 cp_async_arrive(full + slot);
             }
@@ -1179,7 +1187,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                     pos.u = 0;
                     do {
                         ++pos.b;
-                        pos.s = paged_seq(p, pos.b < p.batch ? __ldg(p.lens + pos.b) : 0);
+                        pos.s = paged_seq<C::TT>(p, pos.b < p.batch ? __ldg(p.lens + pos.b) : 0);
                     } while (pos.b < p.batch && pos.s.n == 0);
                 }
             }
@@ -1197,7 +1205,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         PagedSeq s = start.s;
         {
             // What this warp leaves to be joined, and with which CTAs.
-            const PagedPos end = paged_find(p, batch, x0 + tiles - 1);
+            const PagedPos end = paged_find<C::TT>(p, batch, x0 + tiles - 1);
             auto piece = [&](PagedPiece& q, const PagedPos& at, long long tile0, int lo, int hi) {
                 q.b = at.b, q.u = at.u, q.n = at.s.n, q.lo = lo, q.hi = hi;
                 q.c0 = (int)(share_of(total, workers, tile0) / C::NW);
@@ -1229,19 +1237,19 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             }
             const int4 at = meta[slot];
             if (at.z == 0 && done > 0) {
-                s = paged_seq(p, __ldg(p.lens + at.x));
+                s = paged_seq<C::TT>(p, __ldg(p.lens + at.x));
                 state.reset();
                 state.load_q(p, at.x, at.y, lane);
             }
             // Tokens of the set: bit t of the mask.
             const int t = at.w + lane;
             const bool on = t < s.len && ((p.S | p.W) == 0 || t < p.S || t >= s.len - p.W);
-            const unsigned mask = __ballot_sync(0xffffffffu, on);
+            const unsigned mask = __ballot_sync(0xffffffffu, on) & C::kAll;
             unsigned char* stage = ring + slot * C::STAGEB;
-            if (mask != 0xffffffffu) {
+            if (mask != C::kAll) {
                 // Rows of V that do not count may hold anything: zeros, so
                 // that 0 * NaN does not reach the sums.
-                if (!on) {
+                if (!on && lane < C::TT) {
                     for (int g = 0; g < C::SEGS; ++g)
                         for (int c = 0; c < C::SEGB; c += 16)
                             *reinterpret_cast<uint4*>(stage + C::TILEB + C::row(lane) +
@@ -1251,8 +1259,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            const float* sc = scales + slot * 2 * kTile;
-            state.tile(smem_addr(stage), mask, sc, sc + kTile, lane);
+            const float* sc = scales + slot * 2 * C::TT;
+            state.tile(smem_addr(stage), mask, sc, sc + C::TT, lane);
             __syncwarp();
             const bool last = done + 1 == tiles;
             if (issued < tiles) {

@@ -225,6 +225,18 @@ def test_decode(cuda_device, dtype, d, page, hkv, group, lens, n_sink, window, o
     assert torch.equal(_bits(again), _bits(got))
 
 
+@pytest.mark.parametrize("page,token_major", [(8, False), (16, True), (24, False), (64, True)])
+@pytest.mark.parametrize("n_sink,window", [(0, 0), (3, 20), (17, 15), (40, 0), (0, 1)])
+def test_decode_wide_rows(cuda_device, page, token_major, n_sink, window):
+    """fp32 rows of 128 elements come in shorter tiles: ends of sequences, of
+    the sink set and of pages on all sides of theirs."""
+    lens = [15, 16, 17, 0, 31, 32, 33, 49, 700, 1]
+    c = make_cache("f32", lens, page, 3, 128, token_major, seed=page + n_sink)
+    _, q, _, got, lse = _decode(c, lens, 15, 128, F32, n_sink, window, seed=page, dtype="f32")
+    ref = attention(q, c["k64"], c["v64"], lens, n_sink, window)
+    check_attention(got, lse, ref, lens, 128, "f32", F32)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
 def test_decode_many_sequences(cuda_device, dtype):
     """More sequences than warps, most of them short, some empty."""

@@ -120,6 +120,16 @@ def test_decode_refuses(kw, code):
     assert decode(cache(), **kw) == code
 
 
+@pytest.mark.parametrize("c,kw", [
+    (dict(), dict(batch=65535, pages=1 << 20)),
+    (dict(dtype=ab.ALSPEC_F32), dict(batch=65535, pages=1 << 15)),
+    (dict(n_kv_heads=128), dict(hq=128, pages=1 << 27)),
+    (dict(n_kv_heads=1), dict(hq=1024, pages=1 << 27)),
+])
+def test_decode_refuses_more_tiles_than_it_can_number(c, kw):
+    assert decode(cache(**c), **kw) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(x=0), INVALID), (dict(x=P + 8), INVALID), (dict(w=0), INVALID), (dict(w=P + 2), INVALID),
     (dict(y=0), INVALID), (dict(y=P + 1), INVALID), (dict(bias=P + 1), INVALID),
