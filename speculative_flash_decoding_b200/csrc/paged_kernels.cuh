@@ -423,7 +423,14 @@ struct PagedCfg {
     static constexpr int PART = 2 * kHeadRows + kHeadRows * D;  // floats: m, l, o
     static constexpr int kOffHead = NW * ST * STAGEB;  // partials of the warps' first runs
     static constexpr int kOffScale = kOffHead + NW * PART * 4;
-    static constexpr int kOffMeta = kOffScale + (pages_e4m3(T) ? NW * ST * 2 * TT * 4 : 0);
+    // A stage's queries (rows 16 bytes apart, so that their reads meet no
+    // bank twice), for bf16 pages: 123 sequences of 450 tokens 31.2 -> 30.6
+    // us.  The ring of fp32 pages leaves no room, e4m3 pages lost more in
+    // registers (8 x 16K-64K tokens 147 -> 150 us).
+    static constexpr bool kCopyQ = T == kPagesBf16 || T == kPagesBf16Wide;
+    static constexpr int QROW = 2 * D + 16;
+    static constexpr int kOffQ = kOffScale + (pages_e4m3(T) ? NW * ST * 2 * TT * 4 : 0);
+    static constexpr int kOffMeta = kOffQ + (kCopyQ ? NW * ST * kHeadRows * QROW : 0);
     static constexpr int kOffBar = kOffMeta + NW * ST * 16;
     static constexpr int kOffPiece = kOffBar + NW * ST * 8;
     static constexpr int kOffMisc = kOffPiece + 2 * NW * 32;
@@ -652,21 +659,23 @@ struct PagedWarp {
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     }
 
-    // Queries of unit u of sequence b; lanes of absent heads hold zeros.
-    __device__ __forceinline__ void load_q(const PagedParams& p, int b, int u, int lane) {
+    // Queries of unit u of sequence b, of which `rows` copies a stage's rows if
+    // C::kCopyQ; lanes of absent heads hold zeros.
+    __device__ __forceinline__ void load_q(const PagedParams& p, int b, int u,
+                                           const unsigned char* rows, int lane) {
         const int r = lane >> 2, j = lane & 3;
-        const int h0 = (u / p.blocks) * p.group, blk = (u % p.blocks) * kHeadRows;
+        const int blk = (u % p.blocks) * kHeadRows;
         const bool live = blk + r < p.group;
-        const long long at = b * p.q_stride + (long long)(h0 + (live ? blk + r : 0)) * D;
+        const long long at = b * p.q_stride +
+                             (long long)((u / p.blocks) * p.group + (live ? blk + r : 0)) * D;
         rowscale = p.qscale;
         if constexpr (kB16) {
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(
-                static_cast<const __nv_bfloat16*>(p.q) + at);
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(rows + r * C::QROW);
             const uint32_t flip = p.qflip | p.qflip >> 16;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                qa[k][0] = live ? __ldg(q + 8 * k + j) ^ flip : 0u;
-                qa[k][1] = live ? __ldg(q + 8 * k + j + 4) ^ flip : 0u;
+                qa[k][0] = live ? q[8 * k + j] ^ flip : 0u;
+                qa[k][1] = live ? q[8 * k + j + 4] ^ flip : 0u;
             }
         } else if constexpr (pages_e4m3(T)) {
             // Lane j of a quad holds elements 16 k + 4 j .. + 3 of k step k:
@@ -1086,6 +1095,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     unsigned char* ring = smem + warp * C::ST * C::STAGEB;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::ST;
     int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * C::ST;
+    unsigned char* queries = smem + C::kOffQ + warp * (C::ST * kHeadRows * C::QROW);
     float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + warp * C::ST * 2 * C::TT;
     float* deposit0 = reinterpret_cast<float*>(smem + C::kOffHead) + warp * C::PART;
     const int units = p.hkv * p.blocks;
@@ -1145,6 +1155,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             in_page = t - entry * p.page_size;
             if (t < pos.s.len) page = __ldg(p.table + (long long)pos.b * p.max_pages + entry);
         };
+        bool first = true;
         auto issue = [&](int slot) {
             const int left = pos.s.len - t0;  // tokens from here on
             const int h = p.blocks == 1 ? pos.u : pos.u / p.blocks;
@@ -1154,10 +1165,23 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                 atomicOr(p.ctr + kCtrError, kErrPage);
                 page = 0;
             }
+            // The run's queries come with its first tile.
+            const int blk = (pos.u - h * p.blocks) * kHeadRows;
+            const int rows = C::kCopyQ && (first || pos.i == 0) ? min(kHeadRows, p.group - blk) : 0;
+            first = false;
             __syncwarp();
             if (elect_one()) {
                 meta[slot] = make_int4(pos.b, pos.u, pos.i, t0);
-                mbar_arrive_expect_tx(full + slot, (uint32_t)(boxes * box * 2 * C::RB));
+                mbar_arrive_expect_tx(full + slot,
+                                      (uint32_t)(boxes * box * 2 * C::RB + rows * 2 * D));
+            }
+            if constexpr (C::kCopyQ) {
+                __syncwarp();
+                if (lane < rows)
+                    bulk_load(queries + (slot * kHeadRows + lane) * C::QROW,
+                              static_cast<const __nv_bfloat16*>(p.q) + pos.b * p.q_stride +
+                                  (long long)(h * p.group + blk + lane) * D,
+                              2 * D, full + slot, pol);
             }
             for (int i = 0; i < boxes; ++i) {
                 const int pg = __shfl_sync(0xffffffffu, page, i);
@@ -1201,7 +1225,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         PagedWarp<T, D, BOX> state;
         state.init(lane);
         state.reset();
-        state.load_q(p, start.b, start.u, lane);
+        if constexpr (!C::kCopyQ) state.load_q(p, start.b, start.u, nullptr, lane);
         PagedSeq s = start.s;
         {
             // What this warp leaves to be joined, and with which CTAs.
@@ -1239,8 +1263,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             if (at.z == 0 && done > 0) {
                 s = paged_seq<C::TT>(p, __ldg(p.lens + at.x));
                 state.reset();
-                state.load_q(p, at.x, at.y, lane);
             }
+            if (at.z == 0 ? C::kCopyQ || done > 0 : C::kCopyQ && done == 0)
+                state.load_q(p, at.x, at.y, queries + slot * (kHeadRows * C::QROW), lane);
             // Tokens of the set: bit t of the mask.
             const int t = at.w + lane;
             const bool on = t < s.len && ((p.S | p.W) == 0 || t < p.S || t >= s.len - p.W);
