@@ -1352,53 +1352,57 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
     auto head_of = [&](int b, int u) {
         return (long long)b * p.hq + (u / p.blocks) * p.group + (u % p.blocks) * kHeadRows;
     };
-    // A run that began in an earlier CTA is this CTA's first partial, one that
-    // goes on in the next its second.  The 128-element parts of all runs go
-    // round the warps.
-    int open[2] = {-1, -1};  // the pieces that begin them
-    int turn = 0;
-    for (unsigned left = starts; left; left &= left - 1) {
-        const int i = __ffs(left) - 1;
-        const unsigned next = left & (left - 1);
-        const unsigned run = there & ~((1u << i) - 1u) & (next ? (next & -next) - 1u : ~0u);
-        const int lo = __shfl_sync(0xffffffffu, a.lo, i);
-        const int hi = __shfl_sync(0xffffffffu, a.hi, 31 - __clz(run));
-        const bool whole = lo == 0 && hi == __shfl_sync(0xffffffffu, a.n, i);
-        const int part = lo == 0 ? 1 : 0;
-        if (!whole) open[part] = i;
+    // Lane i holds the run that begins with piece i.  One that began in an
+    // earlier CTA is this CTA's first partial, one that goes on in the next
+    // its second.  The runs' parts of 128 elements go round the warps.
+    const bool begins = (starts >> lane) & 1u;
+    const unsigned after = starts & ~((2u << lane) - 1u);
+    const unsigned pieces_of =
+        there & ~((1u << lane) - 1u) & (after ? (after & -after) - 1u : ~0u);
+    const int hi = __shfl_sync(0xffffffffu, a.hi, begins ? 31 - __clz(pieces_of) : lane);
+    const bool whole = a.lo == 0 && hi == a.n;
+    const int part = a.lo == 0 ? 1 : 0;
+    const int open[2] = {__ffs(__ballot_sync(0xffffffffu, begins && !whole && part == 0)) - 1,
+                         __ffs(__ballot_sync(0xffffffffu, begins && !whole && part == 1)) - 1};
+    const int size = begins ? rows_of(a.u) * D : 0;
+    const int parts = (size + 127) / 128;
+    const int incl = warp_inclusive(parts);
+    const int all = __shfl_sync(0xffffffffu, incl, 31);
+    for (int t = warp; t < all; t += C::NW) {
+        const int i = __ffs(__ballot_sync(0xffffffffu, incl > t)) - 1;
+        const int e = (t - __shfl_sync(0xffffffffu, incl - parts, i)) * 128 + 4 * lane;
         const int b = __shfl_sync(0xffffffffu, a.b, i), u = __shfl_sync(0xffffffffu, a.u, i);
-        const int size = rows_of(u) * D;
-        float* mine = p.part + ((long long)blockIdx.x * 2 + part) * C::PART;
-        for (int e0 = 0; e0 < size; e0 += 128, turn = turn + 1 == C::NW ? 0 : turn + 1) {
-            const int e = e0 + 4 * lane, r = e / D;
-            if (turn != warp || e >= size) continue;
-            PagedSum sum;
-            constexpr int kAhead = 4;  // partials on their way together
-            for (unsigned k = run; k;) {
-                float m[kAhead], l[kAhead];
-                float4 o[kAhead];
+        const int end = __shfl_sync(0xffffffffu, size, i);
+        const unsigned run = __shfl_sync(0xffffffffu, pieces_of, i);
+        const int dest = __shfl_sync(0xffffffffu, whole ? -1 : part, i);
+        if (e >= end) continue;
+        const int r = e / D;
+        PagedSum sum;
+        constexpr int kAhead = 4;  // partials on their way together
+        for (unsigned k = run; k;) {
+            float m[kAhead], l[kAhead];
+            float4 o[kAhead];
 #pragma unroll
-                for (int n = 0; n < kAhead; ++n) {
-                    const float* q = partial(k ? __ffs(k) - 1 : i);
-                    m[n] = k ? q[r] : -INFINITY;
-                    l[n] = k ? q[kHeadRows + r] : 0.f;
-                    o[n] = k ? *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-                    k &= k - 1;
-                }
-                sum.add(m, l, o);
+            for (int n = 0; n < kAhead; ++n) {
+                const float* q = partial(k ? __ffs(k) - 1 : i);
+                m[n] = k ? q[r] : -INFINITY;
+                l[n] = k ? q[kHeadRows + r] : 0.f;
+                o[n] = k ? *reinterpret_cast<const float4*>(q + 2 * kHeadRows + e)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                k &= k - 1;
             }
-            if (whole) {
-                sum.write<D>(p, head_of(b, u), e);
-            } else {
-                __stcg(reinterpret_cast<float4*>(mine + 2 * kHeadRows + e), sum.o);
-                if (e % D == 0) {
-                    __stcg(mine + r, sum.m);
-                    __stcg(mine + kHeadRows + r, sum.l);
-                }
+            sum.add(m, l, o);
+        }
+        if (dest < 0) {
+            sum.write<D>(p, head_of(b, u), e);
+        } else {
+            float* mine = p.part + ((long long)blockIdx.x * 2 + dest) * C::PART;
+            __stcg(reinterpret_cast<float4*>(mine + 2 * kHeadRows + e), sum.o);
+            if (e % D == 0) {
+                __stcg(mine + r, sum.m);
+                __stcg(mine + kHeadRows + r, sum.l);
             }
         }
-        __syncwarp();
     }
     if (open[0] < 0 && open[1] < 0) return;
     // The last CTA of a (sequence, unit) to arrive joins it.
