@@ -564,7 +564,7 @@ size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, i
  * Rows behind L_b in the last page may hold anything, NaN included.  Sums and
  * softmax statistics are fp32; results do not depend on timing (no float
  * atomics).  Any group size n_q_heads / n_kv_heads; batch <= 65535, and
- * max_pages * page_size times the batch, or times n_q_heads, below 2^34
+ * max_pages * page_size times the batch, or times n_q_heads, below 2^33
  * (ALSPEC_ERR_UNSUPPORTED from there or a little later on).
  * Asynchronous on `stream`, one launch, no allocation; safe to capture.
  */

@@ -342,9 +342,10 @@ alspec_status alspec_paged_decode(const alspec_paged_cache* cache, const void* q
     const int group = n_q_heads / cache->n_kv_heads;
     const int blocks = (group + kHeadRows - 1) / kHeadRows;
     const int cap = table_tokens(max_pages, cache->page_size);
-    // The running sums of a batch's tiles are 32-bit, and so is a tile's place
-    // among those of a sequence's units.
-    if (std::max<int64_t>(batch, (int64_t)cache->n_kv_heads * blocks) * (cap / kern.tile + 2) >=
+    // The running sums of a batch's costs (two a tile, one a run) are 32-bit,
+    // and so is a place among those of a sequence's units.
+    if (std::max<int64_t>(batch, (int64_t)cache->n_kv_heads * blocks) *
+            (2 * ((int64_t)cap / kern.tile + 2) + 1) >=
         (1ll << 31))
         return ALSPEC_ERR_UNSUPPORTED;
     const int ctas = sm_count_for_plan();

@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 // ---------------------------------------------------------------- decode
 //
 // Every warp of a persistent grid (one CTA per SM) owns an equal share of
-// the batch's tiles of 32 tokens, numbered (sequence, KV head, tile): the
-// share is found from seq_lens alone, so ragged batches are balanced to one
-// tile without a queue.  A warp streams its tiles through a ring of its own
+// the batch's tiles of 32 tokens (16 where rows are long), in the order
+// (sequence, KV head, tile): the share is found from seq_lens alone, so ragged
+// batches are balanced to a tile or so without a queue.  A warp streams its tiles through a ring of its own
 // (TMA boxes of up to 32 rows x 128 bytes, swizzled; it refills a stage as
 // soon as it has read it, so no other warp is waited for) and keeps the
 // running maximum, sum and weighted values of flash decoding.  A (sequence,
@@ -464,19 +464,26 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int len) {
     return s;
 }
 
-// A tile's place: sequence, work unit (KV head and block of 8 query heads).
+// A tile's place: sequence, work unit (KV head and block of 8 query heads),
+// tile of the run, as its tiles of one (sequence, unit) are called.
 struct PagedPos {
     int b, u, i;
     PagedSeq s;
 };
 
-// The batch's tiles: lane i of a warp holds sequences [i * chunk, (i + 1) *
-// chunk), their tiles and the running sum up to their end.
+// What the shares are measured in: two a tile, and one more a run, because
+// starting and ending a run takes a warp about half a tile's time (shares of
+// tiles alone left warps with ten runs of one tile 8 us behind the others).
+// Tile i of a run is at place 2 i + 1 of the run's 2 n + 1.
+__device__ __forceinline__ int paged_cost(int n) { return n > 0 ? 2 * n + 1 : 0; }
+
+// The batch's costs: lane i of a warp holds sequences [i * chunk, (i + 1) *
+// chunk), their cost for one unit and the running sum up to their end.
 struct PagedBatch {
-    int chunk, n, incl;
+    int chunk, cost, incl;
     int len;          // of the lane's sequence, with chunk 1
     int units;
-    long long total;  // tiles of all sequences and units
+    long long total;  // of all sequences and units
 };
 
 __device__ __forceinline__ int warp_inclusive(int x) {
@@ -495,27 +502,27 @@ __device__ __forceinline__ PagedBatch paged_batch(const PagedParams& p) {
     PagedBatch s;
     s.chunk = (p.batch + 31) / 32;
     s.units = p.hkv * p.blocks;
-    s.n = s.len = 0;
+    s.cost = s.len = 0;
 #pragma unroll 4
     for (int b = lane * s.chunk; b < min(p.batch, (lane + 1) * s.chunk); ++b) {
         s.len = __ldg(p.lens + b);
-        s.n += paged_seq<TT>(p, s.len).n;
+        s.cost += paged_cost(paged_seq<TT>(p, s.len).n);
     }
-    s.incl = warp_inclusive(s.n);
+    s.incl = warp_inclusive(s.cost);
     s.total = (long long)__shfl_sync(0xffffffffu, s.incl, 31) * s.units;
     return s;
 }
 
-// The place of tile x (0 <= x < total) in the numbering (sequence, unit,
-// tile); called by a whole warp.
+// Where x (0 <= x < total) lies among the costs in the order (sequence, unit,
+// tile); `i` is the place in the run.  Called by a whole warp.
 template <int TT>
 __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const PagedBatch& t,
                                                long long x) {
     const int lane = threadIdx.x & 31;
     PagedPos r;
     const int w = __ffs(__ballot_sync(0xffffffffu, (long long)t.incl * t.units > x)) - 1;
-    int n = __shfl_sync(0xffffffffu, t.n, w);
-    long long before = __shfl_sync(0xffffffffu, t.incl, w) - n;
+    long long before =
+        __shfl_sync(0xffffffffu, t.incl, w) - __shfl_sync(0xffffffffu, t.cost, w);
     r.b = w;
     if (t.chunk == 1) {
         r.s = paged_seq<TT>(p, __shfl_sync(0xffffffffu, t.len, w));
@@ -524,14 +531,13 @@ __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const Paged
         for (int b0 = w * t.chunk;; b0 += 32) {
             const int b = b0 + lane;
             const bool in = b < min(p.batch, (w + 1) * t.chunk);
-            const int m = in ? paged_seq<TT>(p, __ldg(p.lens + b)).n : 0;
+            const int m = in ? paged_cost(paged_seq<TT>(p, __ldg(p.lens + b)).n) : 0;
             const int incl = warp_inclusive(m);
             const unsigned past =
                 __ballot_sync(0xffffffffu, (before + incl) * t.units > x);
             if (past || b0 + 32 >= (w + 1) * t.chunk) {
                 const int v = past ? __ffs(past) - 1 : 0;
-                n = __shfl_sync(0xffffffffu, m, v);
-                before += __shfl_sync(0xffffffffu, incl, v) - n;
+                before += __shfl_sync(0xffffffffu, incl, v) - __shfl_sync(0xffffffffu, m, v);
                 r.b = b0 + v;
                 break;
             }
@@ -540,13 +546,15 @@ __device__ __forceinline__ PagedPos paged_find(const PagedParams& p, const Paged
         r.s = paged_seq<TT>(p, __ldg(p.lens + r.b));
     }
     const unsigned off = (unsigned)(x - before * t.units);
-    r.u = (int)(off / (unsigned)n);
-    r.i = (int)(off % (unsigned)n);
+    const unsigned cost = (unsigned)paged_cost(r.s.n);
+    r.u = (int)(off / cost);
+    r.i = (int)(off % cost);
     return r;
 }
 
-// Shares: the tiles are spread over `workers` warps, warp w owning
-// [w * total / workers, (w + 1) * total / workers).
+// Shares: the cost is spread over `workers` warps, warp w owning the tiles
+// whose places lie in [w * total / workers, (w + 1) * total / workers).  With
+// two or more each, no share inside a run is without a tile.
 __device__ __forceinline__ long long share_begin(long long total, long long workers, long long w) {
     return w * total / workers;
 }
@@ -554,7 +562,7 @@ __device__ __forceinline__ long long share_of(long long total, long long workers
     return ((x + 1) * workers - 1) / total;
 }
 
-// A run of tiles of one (sequence, unit) that did not end where it began.
+// A warp's part of a run that is not the whole run.
 struct PagedPiece {
     int b, u, lo, hi;  // tiles [lo, hi) of n; hi == 0: none
     int n, c0, c1;     // the CTAs that share the (sequence, unit)
@@ -1115,10 +1123,34 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
 
     const PagedBatch batch = paged_batch<C::TT>(p);
     const long long total = batch.total;
-    const long long workers = min((long long)gridDim.x * C::NW, total);
+    const long long workers = min((long long)gridDim.x * C::NW, total / 2);
     const long long w = (long long)blockIdx.x * C::NW + warp;
     const long long x0 = w < workers ? share_begin(total, workers, w) : 0;
-    const int tiles = w < workers ? (int)(share_begin(total, workers, w + 1) - x0) : 0;
+    const long long x1 = w < workers ? share_begin(total, workers, w + 1) : 0;
+    // The next tile to be issued, and what is left of the share from there on.
+    PagedPos pos{};
+    long long left = 0;
+    auto next_run = [&]() {
+        pos.i = 0;
+        if (++pos.u == units) {
+            pos.u = 0;
+            do {
+                ++pos.b;
+                pos.s = paged_seq<C::TT>(p, pos.b < p.batch ? __ldg(p.lens + pos.b) : 0);
+            } while (pos.b < p.batch && pos.s.n == 0);
+        }
+    };
+    if (w < workers) {
+        // The first tile at or behind x0.
+        pos = paged_find<C::TT>(p, batch, x0);
+        const int place = pos.i;
+        pos.i = place / 2;
+        left = x1 - x0 + place - (2 * pos.i + 1);
+        if (pos.i == pos.s.n) {
+            --left;
+            next_run();
+        }
+    }
     PagedPiece head{}, tail{};
 
     // Padded rows of the batch, and lengths out of range.
@@ -1135,9 +1167,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         }
     };
 
-    if (tiles > 0) {
-        PagedPos pos = paged_find<C::TT>(p, batch, x0);
+    if (left > 0) {
         const PagedPos start = pos;
+        const long long base = x1 - left - (2 * pos.i + 1);  // of its run
         const uint64_t pol = p.blocks == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
         // A tile comes in boxes of `box` rows, K's and V's; lane i keeps the
         // page of box i.
@@ -1157,10 +1189,10 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         };
         bool first = true;
         auto issue = [&](int slot) {
-            const int left = pos.s.len - t0;  // tokens from here on
+            const int tokens = pos.s.len - t0;  // from here on
             const int h = p.blocks == 1 ? pos.u : pos.u / p.blocks;
             unsigned char* stage = ring + slot * C::STAGEB;
-            const int boxes = left >= C::TT ? down : (left + box - 1) / box;
+            const int boxes = tokens >= C::TT ? down : (tokens + box - 1) / box;
             if (sub < boxes && (unsigned)page >= (unsigned)p.n_pages) {
                 atomicOr(p.ctr + kCtrError, kErrPage);
                 page = 0;
@@ -1196,7 +1228,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                 // Lane = token: its scales, and its arrival once they landed.
                 const int pg = __shfl_sync(0xffffffffu, page, from);
                 const int in = __shfl_sync(0xffffffffu, in_page, from) + rem;
-                if (lane < left) {
+                if (lane < tokens) {
                     const long long at = ((long long)pg * p.hkv + h) * p.page_size + in;
                     cp_async_4(scales + slot * 2 * C::TT + lane, p.ks + at);
                     cp_async_4(scales + slot * 2 * C::TT + C::TT + lane, p.vs + at);
@@ -1205,21 +1237,16 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             }
             // On to the next tile; its page numbers are on their way while
             // this one streams.
+            left -= 2;
             if (++pos.i == pos.s.n) {
-                pos.i = 0;
-                if (++pos.u == units) {
-                    pos.u = 0;
-                    do {
-                        ++pos.b;
-                        pos.s = paged_seq<C::TT>(p, pos.b < p.batch ? __ldg(p.lens + pos.b) : 0);
-                    } while (pos.b < p.batch && pos.s.n == 0);
-                }
+                --left;
+                next_run();
             }
             fetch_page();
         };
         fetch_page();
         int issued = 0;
-        for (; issued < min(C::ST, tiles); ++issued) issue(issued);
+        for (; issued < C::ST && left > 0; ++issued) issue(issued);
         __syncwarp();
 
         PagedWarp<T, D, BOX> state;
@@ -1229,23 +1256,26 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         PagedSeq s = start.s;
         {
             // What this warp leaves to be joined, and with which CTAs.
-            const PagedPos end = paged_find<C::TT>(p, batch, x0 + tiles - 1);
-            auto piece = [&](PagedPiece& q, const PagedPos& at, long long tile0, int lo, int hi) {
+            long long y = x1 - 1;
+            PagedPos end = paged_find<C::TT>(p, batch, y);
+            if (end.i == 0) end = paged_find<C::TT>(p, batch, --y);
+            const long long end_base = y - end.i;
+            end.i = (end.i - 1) / 2;
+            auto piece = [&](PagedPiece& q, const PagedPos& at, long long run, int lo, int hi) {
                 q.b = at.b, q.u = at.u, q.n = at.s.n, q.lo = lo, q.hi = hi;
-                q.c0 = (int)(share_of(total, workers, tile0) / C::NW);
-                q.c1 = (int)(share_of(total, workers, tile0 + q.n - 1) / C::NW);
+                q.c0 = (int)(share_of(total, workers, run + 1) / C::NW);
+                q.c1 = (int)(share_of(total, workers, run + 2 * q.n - 1) / C::NW);
             };
             const bool one = end.b == start.b && end.u == start.u;
             const int lo = one ? start.i : 0;
-            if (!one && start.i > 0) piece(head, start, x0 - start.i, start.i, start.s.n);
-            if (lo > 0 || end.i + 1 < end.s.n)
-                piece(tail, end, x0 + tiles - 1 - end.i, lo, end.i + 1);
+            if (!one && start.i > 0) piece(head, start, base, start.i, start.s.n);
+            if (lo > 0 || end.i + 1 < end.s.n) piece(tail, end, end_base, lo, end.i + 1);
         }
         empty_rows();
         int done = 0, slot = 0;
         uint32_t parity = 0;
         bool lost = false, have0 = false, have1 = false;
-        for (; done < tiles; ++done) {
+        for (; done < issued; ++done) {
             // Bounded wait for the fill.
             if (!__all_sync(0xffffffffu, mbar_try_wait(full + slot, parity))) {
                 const uint64_t since = global_ns();
@@ -1287,8 +1317,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             const float* sc = scales + slot * 2 * C::TT;
             state.tile(smem_addr(stage), mask, sc, sc + C::TT, lane);
             __syncwarp();
-            const bool last = done + 1 == tiles;
-            if (issued < tiles) {
+            const bool last = left <= 0 && done + 1 == issued;
+            if (left > 0) {
                 issue(slot);
                 ++issued;
             }
