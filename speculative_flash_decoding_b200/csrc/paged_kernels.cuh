@@ -1451,34 +1451,50 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         misc[threadIdx.x] = last;
     }
     __syncthreads();
+    // Four elements of a run a thread at a time, of more where a run has more
+    // than the CTA has threads: what they read comes from L2, so it is asked
+    // for together.
+    constexpr int kItems = (kHeadRows * D / 4 + C::kThreads - 1) / C::kThreads;
+    constexpr int kAhead = 8;  // partials on their way together
+    const int first = misc[0] ? rows_of(pieces[open[0]].u) * D : 0;
+    const int both = first + (misc[1] ? rows_of(pieces[open[1]].u) * D : 0);
+    for (int x0 = 4 * threadIdx.x; x0 < both; x0 += 4 * kItems * C::kThreads) {
+        int e[kItems], c0[kItems], c1[kItems], longest = 0;
+        long long head0[kItems];
+        PagedSum sum[kItems];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        if (!misc[part]) continue;
-        const PagedPiece& q = pieces[open[part]];
-        const int c0 = q.c0, c1 = q.c1;
-        const long long head0 = head_of(q.b, q.u);
-        for (int e = 4 * threadIdx.x; e < rows_of(q.u) * D; e += 4 * C::kThreads) {
-            const int r = e / D;
-            PagedSum sum;
-            constexpr int kAhead = 8;  // partials on their way together
-            for (int c = c0; c <= c1; c += kAhead) {
-                float m[kAhead], l[kAhead];
-                float4 o[kAhead];
+        for (int n = 0; n < kItems; ++n) {
+            const int x = x0 + 4 * n * C::kThreads;
+            const PagedPiece& q = pieces[x < both ? open[x < first ? 0 : 1] : 0];
+            e[n] = x < first ? x : x - first;
+            c0[n] = q.c0;
+            c1[n] = x < both ? q.c1 : -1;
+            head0[n] = x < both ? head_of(q.b, q.u) : 0;
+            longest = max(longest, c1[n] - c0[n] + 1);
+        }
+        for (int c = 0; c < longest; c += kAhead) {
+            float m[kItems][kAhead], l[kItems][kAhead];
+            float4 o[kItems][kAhead];
+#pragma unroll
+            for (int n = 0; n < kItems; ++n)
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    m[k] = -INFINITY, l[k] = 0.f, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c + k <= c1) {
-                        const float* at =
-                            p.part + ((long long)(c + k) * 2 + (c + k == c0)) * C::PART;
-                        m[k] = __ldcg(at + r);
-                        l[k] = __ldcg(at + kHeadRows + r);
-                        o[k] = __ldcg(reinterpret_cast<const float4*>(at + 2 * kHeadRows + e));
+                    m[n][k] = -INFINITY, l[n][k] = 0.f, o[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int cta = c0[n] + c + k;
+                    if (cta <= c1[n]) {
+                        const float* at = p.part + ((long long)cta * 2 + (c + k == 0)) * C::PART;
+                        m[n][k] = __ldcg(at + e[n] / D);
+                        l[n][k] = __ldcg(at + kHeadRows + e[n] / D);
+                        o[n][k] =
+                            __ldcg(reinterpret_cast<const float4*>(at + 2 * kHeadRows + e[n]));
                     }
                 }
-                sum.add(m, l, o);
-            }
-            sum.write<D>(p, head0, e);
+#pragma unroll
+            for (int n = 0; n < kItems; ++n) sum[n].add(m[n], l[n], o[n]);
         }
+#pragma unroll
+        for (int n = 0; n < kItems; ++n)
+            if (c1[n] >= 0) sum[n].template write<D>(p, head0[n], e[n]);
     }
 }
 
