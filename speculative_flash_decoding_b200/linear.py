@@ -42,9 +42,10 @@ class Linear:
         rows = x.shape[0]
         xt = x.stride()
         if not (x.shape == (rows, self.k) and x.dtype is torch.bfloat16 and x.device == dev
-                and xt[1] == 1):
+                and xt[1] == 1 and (rows <= 1 or xt[0] > 0)):
             raise ValueError(f"x: a bf16 tensor [rows, {self.k}] on {dev} with consecutive "
-                             f"columns is needed, got {x.dtype} {tuple(x.shape)} on {x.device}")
+                             f"columns and rows not broadcast is needed, got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
         if out is None:
             out = torch.empty((rows, n), device=dev,
                               dtype=out_dtype if residual is None else residual.dtype)

@@ -128,8 +128,9 @@ class PagedCache:
         flat = (h * s * d, s * d, d, 1)
         strides = [tuple(c if m == 1 else x for m, x, c in zip(k.shape, t.stride(), flat))
                    for t in (k, v)]
-        _want(strides[0] == strides[1] and strides[0][3] == 1,
-              "k_pages and v_pages need equal strides and consecutive elements in a row")
+        _want(strides[0] == strides[1] and strides[0][3] == 1 and min(strides[0]) > 0,
+              "k_pages and v_pages need equal strides, none of them 0, and consecutive elements "
+              "in a row")
         quantised = k.dtype is torch.float8_e4m3fn
         for name, t in (("k_scales", ks), ("v_scales", vs)):
             if quantised:
@@ -166,10 +167,11 @@ class PagedCache:
         kt, vt = k.stride(), v.stride()
         if not (k.shape == row and v.shape == row and k.dtype in _FLOATS and v.dtype is k.dtype
                 and k.device == dev and v.device == dev and kt[2] == 1 and vt[2] == 1
+                and (n <= 1 or (kt[0] > 0 and vt[0] > 0))
                 and (one_head or (kt[1] == self.head_dim and vt[1] == self.head_dim))):
             raise ValueError("k and v: [n, n_kv_heads, head_dim] tensors in fp32 or bf16 (both "
-                             f"alike) on {dev}, heads side by side, are needed, got "
-                             f"{k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
+                             f"alike) on {dev}, heads side by side, rows not broadcast, "
+                             f"are needed, got {k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
         batch, max_pages = _table(page_table, dev)
         pos = _index(positions, "positions", n, dev)
         seq = 0 if seq_ids is None else _index(seq_ids, "seq_ids", n, dev)
@@ -241,9 +243,9 @@ class PagedDecoder:
         dev, shape = c.device, self._shape
         qt = q.stride()
         if not (q.shape == shape and q.dtype is self.q_dtype and q.device == dev and qt[2] == 1
-                and (shape[1] == 1 or qt[1] == shape[2])):
-            raise ValueError(f"q: {self.q_dtype} {shape} on {dev}, heads side by side, is "
-                             f"needed, got {q.dtype} {tuple(q.shape)} on {q.device}")
+                and (shape[0] == 1 or qt[0] > 0) and (shape[1] == 1 or qt[1] == shape[2])):
+            raise ValueError(f"q: {self.q_dtype} {shape} on {dev}, heads side by side, rows not "
+                             f"broadcast, is needed, got {q.dtype} {tuple(q.shape)} on {q.device}")
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=dev)
         elif not (out.shape == shape and out.dtype in _FLOATS and out.device == dev

@@ -121,6 +121,16 @@ def test_activation_far_out(cuda_device):
         assert bool(((y.double() - want).abs() <= 2.0 ** -20 * x.double().abs()).all()), act
 
 
+def test_broadcast_rows_are_refused(cuda_device):
+    """A stride of 0 means contiguous rows to the C entry point."""
+    from speculative_flash_decoding_b200 import Linear
+    lin = Linear(torch.zeros(16, 64, dtype=torch.bfloat16, device="cuda"))
+    x = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="broadcast"):
+        lin.apply(x.expand(5, 64))
+    assert lin.apply(x.expand(1, 64)).shape == (1, 16)
+
+
 def test_no_rows(cuda_device):
     from speculative_flash_decoding_b200 import Linear
     _, w, b, _ = _inputs(1, 64, 64)

@@ -449,6 +449,27 @@ def test_decode_on_two_streams_at_once(cuda_device):
         check_attention(o, None, attention(q, c["k64"], c["v64"], lens), lens, 64, "bf16", F32)
 
 
+def test_broadcast_rows_are_refused(cuda_device):
+    """A stride of 0 means contiguous rows to the C entry points."""
+    from speculative_flash_decoding_b200 import PagedCache, PagedDecoder
+    cache = PagedCache(8, 16, 2, 64)
+    table = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    one = torch.zeros((1, 2, 64), dtype=BF16, device="cuda")
+    for k, v in ((one.expand(3, 2, 64), one.repeat(3, 1, 1)),
+                 (one.repeat(3, 1, 1), one.expand(3, 2, 64))):
+        with pytest.raises(ValueError, match="broadcast"):
+            cache.append(k, v, pos, table)
+    with pytest.raises(ValueError, match="broadcast"):
+        PagedDecoder(cache, 3, 2).decode(one.expand(3, 2, 64), table, pos)
+    pool = one.reshape(2, 1, 1, 64)[:1].expand(4, 2, 16, 64)
+    with pytest.raises(ValueError, match="strides"):
+        PagedCache.from_tensors(pool, pool)
+    # One row has no stride to be broadcast by.
+    cache.append(one.expand(1, 2, 64), one, pos[:1], table[:1])
+    assert cache.device_error() == (0, 0)
+
+
 def test_offsets_past_32_bits(cuda_device):
     """Pages whose element offsets pass 2^32: written, read back, attended."""
     from speculative_flash_decoding_b200 import PagedCache, PagedDecoder
