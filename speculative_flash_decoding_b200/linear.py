@@ -6,7 +6,7 @@ import torch
 
 from . import alspec as _c
 from .alspec import AlspecError
-from .paged import _CODES, _FLOATS, _on, _stream, _take_error, _want
+from .paged import _CODES, _FLOATS, _empty, _on, _settle, _stream, _take_error, _want
 
 
 class Linear:
@@ -32,12 +32,13 @@ class Linear:
         self.activation = _c.ACTIVATIONS[activation]
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._index = self.device.index
+        _settle(self.device)
 
     def apply(self, x, residual=None, out=None, out_dtype=torch.bfloat16, stream=None):
         """x bf16 [rows, k] (rows may be slices of wider ones); residual, if
         given, and out are contiguous [rows, n] tensors of one type (fp32 or
         bf16; ``out_dtype`` where out is to be made) and may be the same
-        tensor.  Returns out."""
+        tensor.  Returns out; a new one belongs to the stream of the call."""
         dev, n = self.device, self.n
         rows = x.shape[0]
         xt = x.stride()
@@ -47,8 +48,8 @@ class Linear:
                              f"columns and rows not broadcast is needed, got {x.dtype} "
                              f"{tuple(x.shape)} on {x.device}")
         if out is None:
-            out = torch.empty((rows, n), device=dev,
-                              dtype=out_dtype if residual is None else residual.dtype)
+            out = _empty((rows, n), out_dtype if residual is None else residual.dtype, dev,
+                         stream)
         if not (out.shape == (rows, n) and out.dtype in _FLOATS and out.device == dev
                 and out.is_contiguous()):
             raise ValueError(f"out: a contiguous tensor [{rows}, {n}] in fp32 or bf16 on {dev} "

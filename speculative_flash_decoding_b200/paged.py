@@ -46,6 +46,21 @@ def _on(index, fn, *args):
         return fn(*args)
 
 
+def _empty(shape, dtype, device, stream):
+    """An output made for a call on `stream`: from that stream's memory, so
+    that nothing earlier on the current one still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _settle(device):
+    """What a constructor has zeroed is there for calls on any stream."""
+    if not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+
+
 def _want(ok, what):
     if not ok:
         raise ValueError(what)
@@ -153,6 +168,7 @@ class PagedCache:
         # Sizes and strides that no entry point takes are refused here.
         if _c.alspec_paged_workspace_size(self.desc, 1, h) == 0:
             raise AlspecError(_c.ALSPEC_ERR_UNSUPPORTED, "alspec_paged_workspace_size")
+        _settle(self.device)
 
     def append(self, k, v, positions, page_table, seq_ids=None, stream=None):
         """Write new tokens' rows: k, v [n, n_kv_heads, head_dim] (fp32 or
@@ -171,7 +187,8 @@ class PagedCache:
                 and (one_head or (kt[1] == self.head_dim and vt[1] == self.head_dim))):
             raise ValueError("k and v: [n, n_kv_heads, head_dim] tensors in fp32 or bf16 (both "
                              f"alike) on {dev}, heads side by side, rows not broadcast, "
-                             f"are needed, got {k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
+                             f"are needed, got {k.dtype} {tuple(k.shape)} and {v.dtype} "
+                             f"{tuple(v.shape)}")
         batch, max_pages = _table(page_table, dev)
         pos = _index(positions, "positions", n, dev)
         seq = 0 if seq_ids is None else _index(seq_ids, "seq_ids", n, dev)
@@ -232,13 +249,15 @@ class PagedDecoder:
         self.workspace_bytes = nbytes
         self.q_dtype = torch.float32 if cache.dtype is torch.float32 else torch.bfloat16
         self._shape = (self.batch, self.n_q_heads, cache.head_dim)
+        _settle(cache.device)
 
     def decode(self, q, page_table, seq_lens, out=None, lse=None, stream=None):
         """q [batch, n_q_heads, head_dim] (fp32 for fp32 pages, else bf16;
         rows may be slices of wider ones) over sequence b's first
         seq_lens[b] tokens (0: zeros), or with n_sink + window > 0 over its
         sink set.  Fills out (fp32 or bf16; new: q's type) and, if given, lse
-        (fp32 [batch, n_q_heads], natural logarithm); returns out."""
+        (fp32 [batch, n_q_heads], natural logarithm); returns out.  A new out
+        belongs to the stream of the call."""
         c = self.cache
         dev, shape = c.device, self._shape
         qt = q.stride()
@@ -247,7 +266,7 @@ class PagedDecoder:
             raise ValueError(f"q: {self.q_dtype} {shape} on {dev}, heads side by side, rows not "
                              f"broadcast, is needed, got {q.dtype} {tuple(q.shape)} on {q.device}")
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            out = _empty(shape, q.dtype, dev, stream)
         elif not (out.shape == shape and out.dtype in _FLOATS and out.device == dev
                   and out.is_contiguous()):
             raise ValueError(f"out: a contiguous fp32 or bf16 tensor {shape} on {dev} is needed, "

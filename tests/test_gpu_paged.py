@@ -449,6 +449,31 @@ def test_decode_on_two_streams_at_once(cuda_device):
         check_attention(o, None, attention(q, c["k64"], c["v64"], lens), lens, 64, "bf16", F32)
 
 
+def test_new_output_comes_from_the_memory_of_its_stream(cuda_device):
+    """Freed memory that the current stream still writes is not handed to a
+    call on another stream."""
+    from speculative_flash_decoding_b200 import Linear, PagedCache, PagedDecoder
+    side = torch.cuda.Stream()
+    lin = Linear(torch.ones(4096, 64, dtype=BF16, device="cuda"))
+    x = torch.ones(64, 64, dtype=BF16, device="cuda")
+    dec = PagedDecoder(PagedCache(8, 16, 2, 64), 64, 64)
+    q = torch.ones((64, 64, 64), dtype=BF16, device="cuda")
+    table = torch.zeros((64, 1), dtype=torch.int32, device="cuda")
+    lens = torch.zeros(64, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for shape, call, value in (((64, 4096), lambda: lin.apply(x, stream=side), 64.0),
+                               ((64, 64, 64), lambda: dec.decode(q, table, lens, stream=side), 0.0)):
+        old = torch.empty(shape, dtype=BF16, device="cuda")
+        at = old.data_ptr()
+        torch.cuda._sleep(20_000_000)  # some milliseconds
+        old.fill_(7.0)
+        del old
+        out = call()
+        assert out.data_ptr() != at
+        torch.cuda.synchronize()
+        assert torch.equal(out, torch.full_like(out, value))
+
+
 def test_broadcast_rows_are_refused(cuda_device):
     """A stride of 0 means contiguous rows to the C entry points."""
     from speculative_flash_decoding_b200 import PagedCache, PagedDecoder
