@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -200,14 +201,6 @@ __device__ __forceinline__ void lin_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void lin_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Four neighbouring values, aligned to their size.
-__device__ __forceinline__ float4 lin_value4(const float* p) {
-    return *reinterpret_cast<const float4*>(p);
-}
-__device__ __forceinline__ float4 lin_value4(const __nv_bfloat16* p) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
-                       __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
-}
 __device__ __forceinline__ void lin_put4(float* p, const float* v) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -217,9 +210,17 @@ __device__ __forceinline__ void lin_put4(__nv_bfloat16* p, const float* v) {
 
 // The epilogue of batch rows [c0, c1) of a tile.  Their sums lie in shared
 // memory, either one part in each of the cluster's CTAs (of its half, where
-// CTAS is 2), [row][feature], or (PUSH) all parts here, [CTA][row - c0][feature].  A warp takes a row at a
-// time, a lane four features; everything a round of R rows needs is asked for
-// before it is used (rounds of four rows: 44.1 us for 250 x 8192 x 8192).
+// CTAS is 2), [row][feature], or (PUSH) all parts here, [CTA][row - c0]
+// [feature].  A warp takes a row at a time, a lane four features; a round of R
+// rows is asked for (the residual, the first two parts) before the round ahead
+// is finished (250 x 8192 x 8192 36.2 -> 35.7 us, 33 x 4096 x 6144 14.7 ->
+// 14.5; large batches take rounds of eight rows, with four 36.1).
+template <typename O, int R>
+struct LinRound {
+    alignas(16) O add[R][4];  // the residual
+    float4 part[2][R];
+};
+
 template <typename O, bool PUSH, int CTAS, int R>
 __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sums, int place,
                                              int c0, int c1, int r0, int n0) {
@@ -228,6 +229,45 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
     const int f = n0 + 4 * lane;
     const int nf = min(4, p.n - f);  // features of this lane
     if (nf <= 0) return;
+    const O* res = static_cast<const O*>(p.residual);
+    const long long step = (long long)kWarps * p.n;
+    // Part s of row c + u * kWarps, u < R.
+    auto load_part = [&](int c, int s, float4 (&part)[R]) {
+        const uint32_t here = sums + (uint32_t)((PUSH ? c - c0 : c) * kLinM + 4 * lane) * 4;
+        // This CTA's own part without the way through the cluster.
+        if (PUSH || s == place / CTAS) {
+            const uint32_t from = here + (uint32_t)(PUSH ? s * p.slice * kLinM * 4 : 0);
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                if (c + u * kWarps < c1) part[u] = lds_v4(from + u * kWarps * kLinM * 4);
+        } else {
+            const uint32_t from = dsmem_addr(here, (uint32_t)(s * CTAS + place % CTAS));
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
+        }
+    };
+    auto load = [&](int c, LinRound<O, R>& r) {
+        if (res) {
+            const O* from = res + (long long)(r0 + c) * p.n + f;
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                if (c + u * kWarps >= c1) continue;
+                if (p.vec) {
+                    using V = typename std::conditional<sizeof(O) == 4, float4, uint2>::type;
+                    *reinterpret_cast<V*>(r.add[u]) = *reinterpret_cast<const V*>(from + u * step);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < nf) r.add[u][i] = from[u * step + i];
+                }
+            }
+        }
+        load_part(c, 0, r.part[0]);
+        if (p.split > 1) load_part(c, 1, r.part[1]);
+    };
+    LinRound<O, R> now;
+    if (c0 + warp < c1) load(c0 + warp, now);
     float bias[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.bias) {
 #pragma unroll
@@ -235,67 +275,47 @@ __device__ __forceinline__ void lin_epilogue(const LinearParams& p, uint32_t sum
             if (i < nf) bias[i] = __bfloat162float(p.bias[f + i]);
     }
     for (int c = c0 + warp; c < c1; c += kWarps * R) {
-        const long long at = (long long)(r0 + c) * p.n + f;
-        const long long step = (long long)kWarps * p.n;
-        const O* res = static_cast<const O*>(p.residual);
-        float v[4 * R], add[4 * R];
-        if (res) {
+        LinRound<O, R> next;
+        if (c + kWarps * R < c1) load(c + kWarps * R, next);
+        float v[4 * R];
+        auto add_part = [&](const float4 (&part)[R]) {
 #pragma unroll
             for (int u = 0; u < R; ++u) {
-                if (c + u * kWarps >= c1) continue;
-                if (p.vec) {
-                    const float4 x = lin_value4(res + at + u * step);
-                    add[4 * u] = x.x, add[4 * u + 1] = x.y, add[4 * u + 2] = x.z, add[4 * u + 3] = x.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < nf) add[4 * u + i] = lin_value(res + at + u * step + i);
-                }
+                v[4 * u] += part[u].x, v[4 * u + 1] += part[u].y;
+                v[4 * u + 2] += part[u].z, v[4 * u + 3] += part[u].w;
             }
+        };
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            v[4 * u] = now.part[0][u].x, v[4 * u + 1] = now.part[0][u].y;
+            v[4 * u + 2] = now.part[0][u].z, v[4 * u + 3] = now.part[0][u].w;
         }
-        const uint32_t here =
-            sums + (uint32_t)((PUSH ? c - c0 : c) * kLinM + 4 * lane) * 4;
-        for (int s = 0; s < p.split; ++s) {
-            // This CTA's own part without the way through the cluster.
+        if (p.split > 1) add_part(now.part[1]);
+        for (int s = 2; s < p.split; ++s) {
             float4 part[R];
-            if (PUSH || s == place / CTAS) {
-                const uint32_t from = here + (uint32_t)(PUSH ? s * p.slice * kLinM * 4 : 0);
-#pragma unroll
-                for (int u = 0; u < R; ++u)
-                    if (c + u * kWarps < c1) part[u] = lds_v4(from + u * kWarps * kLinM * 4);
-            } else {
-                const uint32_t from = dsmem_addr(here, (uint32_t)(s * CTAS + place % CTAS));
-#pragma unroll
-                for (int u = 0; u < R; ++u)
-                    if (c + u * kWarps < c1) part[u] = ld_dsmem_v4(from + u * kWarps * kLinM * 4);
-            }
-#pragma unroll
-            for (int u = 0; u < R; ++u) {
-                v[4 * u] = s ? v[4 * u] + part[u].x : part[u].x;
-                v[4 * u + 1] = s ? v[4 * u + 1] + part[u].y : part[u].y;
-                v[4 * u + 2] = s ? v[4 * u + 2] + part[u].z : part[u].z;
-                v[4 * u + 3] = s ? v[4 * u + 3] + part[u].w : part[u].w;
-            }
+            load_part(c, s, part);
+            add_part(part);
         }
 #pragma unroll
         for (int i = 0; i < 4 * R; ++i) v[i] += bias[i % 4];
         lin_activate(v, p.act);
         if (res) {
 #pragma unroll
-            for (int i = 0; i < 4 * R; ++i) v[i] += add[i];
+            for (int i = 0; i < 4 * R; ++i) v[i] += lin_value(&now.add[i / 4][i % 4]);
         }
-        O* y = static_cast<O*>(p.y);
+        O* y = static_cast<O*>(p.y) + (long long)(r0 + c) * p.n + f;
 #pragma unroll
         for (int u = 0; u < R; ++u) {
             if (c + u * kWarps >= c1) continue;
             if (p.vec) {
-                lin_put4(y + at + u * step, v + 4 * u);
+                lin_put4(y + u * step, v + 4 * u);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (i < nf) lin_put(y + at + u * step + i, v[4 * u + i]);
+                    if (i < nf) lin_put(y + u * step + i, v[4 * u + i]);
             }
         }
+        now = next;
     }
 }
 
