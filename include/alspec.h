@@ -563,7 +563,12 @@ size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, i
  *   timeout_ms  bound on any in-kernel wait; 0 = 2000
  * Rows behind L_b in the last page may hold anything, NaN included.  Sums and
  * softmax statistics are fp32; results do not depend on timing (no float
- * atomics).  Any group size n_q_heads / n_kv_heads; batch <= 65535, and
+ * atomics).  What is held in fewer bits on the way: over ALSPEC_BF16 pages a
+ * probability in 16 bits for bf16 outputs, 24 for fp32; over ALSPEC_E4M3 pages
+ * a probability times its V scale in 22 bits, or to 2^-36 of the largest such
+ * product so far where that is coarser, and a query element to 2^-25 of its
+ * head's largest where that is coarser than bf16; over ALSPEC_F32 pages
+ * queries, keys, values and probabilities in 22 bits.  Any group size n_q_heads / n_kv_heads; batch <= 65535, and
  * max_pages * page_size times the batch, or times n_q_heads, below 2^33
  * (ALSPEC_ERR_UNSUPPORTED from there or a little later on).
  * Asynchronous on `stream`, one launch, no allocation; safe to capture.

@@ -345,9 +345,10 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 //   bf16 pages  Q is exact; P = hi + lo (16 bits), for fp32 outputs a third
 //               bf16 term in a second MMA (24 bits);
 //   e4m3 pages  codes widen exactly to f16; Q, scaled by a power of two per
-//               head, is f16 (its bf16 fit), P f16 hi + lo (22 bits).  The K scale
-//               multiplies a score, the V scale a probability, which is kept
-//               in f16's range by a running power of two (vexp);
+//               head, is f16 (its bf16 fit).  The K scale multiplies a score,
+//               the V scale a probability; the product, a weight, is f16
+//               hi + lo over a power of two that follows the largest weight
+//               so far (wexp): 22 bits, or 2^-36 of that largest;
 //   fp32 pages  tf32 with hi + lo of both operands (22 bits).
 // Bound by HBM bytes over bf16 pages (128K tokens of 8 KV heads: 84 us, 6.4
 // TB/s), by instructions over e4m3 pages (8 x 16K-64K tokens: 147 us, 5.3 TB/s;
@@ -595,6 +596,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// 1 / x for a power of two in [2^-126, 2^126].
+__device__ __forceinline__ float pow2_inverse(float x) {
+    return __uint_as_float(0x7f000000u - __float_as_uint(x));
+}
+
 // Partials of one head joined: running maximum, sum, four weighted values.
 struct PagedSum {
     float m = -INFINITY, l = 0.f;
@@ -648,7 +654,7 @@ struct PagedWarp {
     float acc[NT][4];                      // rows 0-7 and 8-15
     float m, l;                            // this lane's head: maximum, share of the sum
     float rowscale;                        // log2-domain factor of a score
-    float vexp;                            // e4m3: acc holds sums times 1 / vexp
+    float wexp;                            // e4m3: acc holds sums times 1 / wexp
     uint32_t k_off, v_off;                 // this lane's part of a fragment's address
 
     __device__ __forceinline__ void init(int lane) {
@@ -664,7 +670,7 @@ struct PagedWarp {
     __device__ __forceinline__ void reset() {
         m = -INFINITY;
         l = 0.f;
-        vexp = kMinScale;
+        wexp = kMinScale;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -833,7 +839,7 @@ struct PagedWarp {
         }
         // Lane (r, j) holds head r, tokens 8 n + 2 j and + 1.  x: scores, up
         // to the factor `f` that makes them logarithms to base 2.
-        float x[NG][2], vsc[NG][2], vmax = 0.f, f = rowscale;
+        float x[NG][2], vsc[NG][2], f = rowscale;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -867,36 +873,75 @@ struct PagedWarp {
         const float m_new = mx > m + 8.f ? mx : m;
         const float base = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = m == m_new ? 1.f : fast_exp2(m - base);
-        float rescale = alpha, vinv = 1.f;
+        // e4m3: the V scales over the weights' power of two.
+        float sv[pages_e4m3(T) ? NG : 1][2], over = 0.f;
         if constexpr (pages_e4m3(T)) {
+            const float winv = pow2_inverse(wexp);
 #pragma unroll
-            for (int n = 0; n < NG; ++n) vmax = fmaxf(vmax, fmaxf(fabsf(vsc[n][0]), fabsf(vsc[n][1])));
-            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-            // The power of two at or below the largest V scale so far; 1 /
-            // vexp by its exponent (halved where that is past the range).
-            const float v2 = fmaxf(
-                vexp, __uint_as_float(min(__float_as_uint(vmax), 0x7f000000u) & 0x7f800000u));
-            if (v2 != vexp) rescale = alpha * (vexp / v2);
-            vexp = v2;
-            const uint32_t e = __float_as_uint(v2);
-            vinv = e == 0x7f000000u ? 5.877471754e-39f : __uint_as_float(0x7f000000u - e);
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    sv[n][i] = vsc[n][i] * winv;
+                    over = fmaxf(over, fabsf(sv[n][i]));
+                }
         }
-        float sum = 0.f;
+        const bool again = alpha != 1.f || over == INFINITY;
+        float sum = 0.f, wmax = 0.f;
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 x[n][i] = fast_exp2(fmaf(x[n][i], f, -base));
                 sum += x[n][i];
-                if constexpr (pages_e4m3(T)) x[n][i] *= vsc[n][i] * vinv;
+                if constexpr (pages_e4m3(T)) {
+                    sv[n][i] *= x[n][i];
+                    wmax = fmaxf(wmax, fabsf(sv[n][i]));
+                }
             }
+        float rescale = alpha;
+        // f16 ends at 2^-24, and neither the largest probability nor the
+        // largest V scale says how large the largest weight is (an attention
+        // sink has a small value, an outlier hardly any probability), so the
+        // weights' own maximum sets their power of two: to 2^11 .. 2^12 of it
+        // when the probabilities' reference moves up past what came before,
+        // and when a weight passes 2^15.
+        const bool moved = (!kApart || pages_e4m3(T)) &&
+                           __any_sync(0xffffffffu, again || wmax > 32768.f);
+        if constexpr (pages_e4m3(T)) {
+            if (moved) {
+                wmax = 0.f;
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        sv[n][i] = x[n][i] * vsc[n][i];
+                        wmax = fmaxf(wmax, fabsf(sv[n][i]));
+                    }
+                wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, 1));
+                wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, 2));
+                const float now = wexp * alpha;
+                const float to = wmax > now * 32768.f ? wmax * (1.f / 2048.f) : now;
+                // (In [2^-126, 2^126], so that 1 / wexp is a normal number.)
+                wexp = __uint_as_float(
+                    min(max(__float_as_uint(to) & 0x7f800000u, 0x00800000u), 0x7e800000u));
+                const float winv = pow2_inverse(wexp);
+                rescale = now * winv;
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) sv[n][i] *= winv;
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x[n][i] = sv[n][i];
+        }
         m = m_new;
         l = l * alpha + sum;
         // For fp32 outputs a tile's products are summed apart and then added,
         // because the MMAs' sums lose towards zero (one chain over all of a
         // warp's tiles: 1.8e-5 of the result at 2 x 16 x 55854 fp32 tokens).
-        if (!kApart && __any_sync(0xffffffffu, rescale != 1.f)) {
+        if (!kApart && moved) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -1050,8 +1095,8 @@ struct PagedWarp {
             for (int k = 0; k < 2; ++k) {
                 if constexpr (pages_e4m3(T)) {
                     // Tiles i and i + 1 hold the even and odd columns of 16.
-                    f(8 * i + 4 * j + 2 * k, (acc[i][k] + acc[i][k + 2]) * vexp,
-                      (acc[i + 1][k] + acc[i + 1][k + 2]) * vexp);
+                    f(8 * i + 4 * j + 2 * k, (acc[i][k] + acc[i][k + 2]) * wexp,
+                      (acc[i + 1][k] + acc[i + 1][k + 2]) * wexp);
                 } else {
                     f(8 * (i + k) + 2 * j, acc[i + k][0] + acc[i + k][2],
                       acc[i + k][1] + acc[i + k][3]);
