@@ -568,7 +568,10 @@ size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, i
  * a probability times its V scale in 22 bits, or to 2^-36 of the largest such
  * product so far where that is coarser, and a query element to 2^-25 of its
  * head's largest where that is coarser than bf16; over ALSPEC_F32 pages
- * queries, keys, values and probabilities in 22 bits.  Any group size n_q_heads / n_kv_heads; batch <= 65535, and
+ * queries, keys, values and probabilities to 2^-21.4.  A NaN among the
+ * queries, keys and values attended to reaches every output that reads it; an
+ * infinity makes NaN or an infinity there, except that a key with a score of
+ * -inf may count as absent.  Any group size n_q_heads / n_kv_heads; batch <= 65535, and
  * max_pages * page_size times the batch, or times n_q_heads, below 2^33
  * (ALSPEC_ERR_UNSUPPORTED from there or a little later on).
  * Asynchronous on `stream`, one launch, no allocation; safe to capture.

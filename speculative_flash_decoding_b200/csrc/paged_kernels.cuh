@@ -349,11 +349,11 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 //               the V scale a probability; the product, a weight, is f16
 //               hi + lo over a power of two that follows the largest weight
 //               so far (wexp): 22 bits, or 2^-36 of that largest;
-//   fp32 pages  tf32 with hi + lo of both operands (22 bits).
+//   fp32 pages  tf32 with hi + lo of both operands (2^-21.4).
 // Bound by HBM bytes over bf16 pages (128K tokens of 8 KV heads: 84 us, 6.4
 // TB/s), by instructions over e4m3 pages (8 x 16K-64K tokens: 147 us, 5.3 TB/s;
 // a tile of 8 KB takes 128 conversions and 64 MMAs) and fp32 pages (4 x 20000
-// tokens of 128 elements: 125-131 us, 5.1 TB/s), by the reads before the first
+// tokens of 128 elements: 122-124 us, 5.3 TB/s), by the reads before the first
 // tile and the joins after the last where the sequences are short (123 of
 // 1-900 tokens: 30 us for 17.6 us of bytes).
 
@@ -753,11 +753,15 @@ struct PagedWarp {
         y -= __uint_as_float(hi & 0xffff0000u);
         return hi;
     }
-    // hi + lo = x to 22 bits, both rounded to nearest (the MMA ignores the
-    // low 13 bits of lo).
+    // hi + lo = x to 2^-21.4: hi is x cut off, lo the rest, of which the MMA
+    // ignores the low 13 bits; the factor raises lo by 0.36 .. 0.72 of what
+    // they stand for, half a step on the average.  No integer addition: it
+    // would carry a NaN's payload into the sign (the NaN of fp32 arithmetic is
+    // 0x7fffffff) and the largest finite values into infinity.  A NaN whose
+    // payload is in the low bits alone leaves hi infinite, but lo NaN.
     __device__ __forceinline__ static void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-        hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-        lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+        hi = __float_as_uint(x) & 0xffffe000u;
+        lo = __float_as_uint((x - __uint_as_float(hi)) * (1.f + 0x1.7p-12f));
     }
 
     __device__ __forceinline__ static float lds(uint32_t addr) {

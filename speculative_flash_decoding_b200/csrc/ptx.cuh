@@ -164,7 +164,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
 }
 
 // D(16x8 fp32) += A(16x8 tf32, row) * B(8x8 tf32, col); the operands are fp32
-// words whose low 13 bits are zero.
+// words whose low 13 bits are ignored.
 __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(

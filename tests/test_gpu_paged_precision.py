@@ -86,3 +86,75 @@ def test_v_scales_over_a_wide_range(cuda_device, out_dtype):
     bound, _ = attention_bound(ref, lens, 64, "e4m3", out_dtype)
     err = (got.double().cpu() - ref[0]).abs()
     assert bool((err <= bound).all()), float((err / bound).max())
+
+
+# NaN as fp32 arithmetic makes it (0x7fffffff), as math.nan (0x7fc00000), with
+# the least payload, and negative ones.
+NANS = [0x7fffffff, 0x7fc00000, 0x7ffff000, 0x7f800001, -1, -(0x7fffff)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", NANS)
+def test_every_nan_reaches_its_heads_over_fp32_pages(cuda_device, d, bits):
+    from speculative_flash_decoding_b200 import PagedCache, PagedDecoder
+    lens = [200, 150, 40]
+    c = make_cache("f32", lens, 16, 2, d, seed=2)
+    q = torch.randn(3, 4, d, generator=torch.Generator().manual_seed(0)).cuda()
+
+    def poke(x, *at):
+        x.view(torch.int32)[at] = bits
+
+    for name, b, h, t in (("k", 0, 1, 100), ("v", 1, 0, 100)):
+        poke(c[name], c["table"][b, t // 16].long(), h, t % 16, 5)
+    poke(q, 2, 3, 7)
+    dec = PagedDecoder(PagedCache.from_tensors(c["k"], c["v"]), 3, 4)
+    lse = torch.empty(3, 4, device="cuda")
+    out = dec.decode(q, c["table"], torch.tensor(lens, dtype=torch.int32, device="cuda"), lse=lse)
+    bad = torch.zeros(3, 4, d, dtype=torch.bool, device="cuda")
+    bad[0, 2:] = True     # a NaN key
+    bad[1, :2, 5] = True  # a NaN value
+    bad[2, 3] = True      # a NaN query
+    assert torch.equal(out.isnan(), bad)
+    of_scores = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+    of_scores[0, 2:] = of_scores[2, 3] = True
+    assert torch.equal(lse.isnan(), of_scores)
+
+
+@pytest.mark.parametrize("bits", [0x7f7fffff, 0x7f7ff000, 0x7f7fefff, 0x7f7fe000])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_values_near_the_largest_over_fp32_pages(cuda_device, bits, sign):
+    """Finite keys, values and queries up to the largest fp32 stay finite:
+    here a key meets a query element of 2^-124, a value a weight of e^-60, a
+    query element keys of 2^-112."""
+    from speculative_flash_decoding_b200 import PagedCache, PagedDecoder
+    d, lens = 64, [150, 90, 40]
+    big = sign * float(torch.tensor(bits, dtype=torch.int32).view(torch.float32))
+    c = make_cache("f32", lens, 16, 1, d, seed=5)
+    q = torch.randn(3, 4, d, generator=torch.Generator().manual_seed(3))
+
+    def put(name, b, t, e, x):
+        c[name][c["table"][b, t // 16].long(), 0, t % 16, e] = x
+        c[name + "64"][b, 0, t, e] = x
+
+    q[0, :, 5] = 2.0 ** -124
+    put("k", 0, 100, 5, big)
+    q[1] = q[1, :1]  # heads alike, so that one key is at -60 for all
+    u = q[1, 0].clone()
+    for e in range(d):
+        put("k", 1, 30, e, float(-60.0 * math.sqrt(d) * u[e] / (u @ u)))
+    put("v", 1, 30, 9, big)
+    q[2] *= 2.0 ** 16
+    q[2, :, 7] = big
+    for t in range(lens[2]):
+        put("k", 2, t, 7, float(c["k64"][2, 0, t, 7] * 2.0 ** -112))
+        for e in range(d):
+            if e != 7:
+                put("k", 2, t, e, float(c["k64"][2, 0, t, e] * 2.0 ** -16))
+    q = q.cuda()
+    dec = PagedDecoder(PagedCache.from_tensors(c["k"], c["v"]), 3, 4)
+    got = dec.decode(q, c["table"], torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    ref = attention(q, c["k64"], c["v64"], lens)
+    bound, _ = attention_bound(ref, lens, d, "f32", F32)
+    err = (got.double().cpu() - ref[0]).abs()
+    assert bool(got.isfinite().all())
+    assert bool((err <= bound).all()), float((err / bound).max())
