@@ -542,9 +542,12 @@ size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, i
  *               and bf16 otherwise, 16-byte aligned; sequence b's row starts
  *               at b * q_stride elements (0: contiguous), whose byte count is
  *               a multiple of 16
- *   page_table  device int32 [batch][max_pages]; entries behind a sequence's
- *               last page are not read.  An entry outside [0, n_pages) sets
- *               ALSPEC_DEVERR_PAGE and that sequence's output is undefined.
+ *   page_table  device int32 [batch][max_pages]; entries of pages that hold
+ *               no token attended to are not read (those behind a sequence's
+ *               last page; with n_sink + window > 0 also those between the
+ *               first n_sink tokens and the last window).  Of the others one
+ *               outside [0, n_pages) sets ALSPEC_DEVERR_PAGE and that
+ *               sequence's output is undefined.
  *   seq_lens    device int32 [batch], 0 <= L_b <= max_pages * page_size; out
  *               of range: clamped, ALSPEC_DEVERR_SEQ_LEN.  A sequence of
  *               length 0 (a padded row of the batch) gets zeros, and -inf in

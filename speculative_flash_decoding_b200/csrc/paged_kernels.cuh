@@ -1233,20 +1233,25 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
         int page = 0;    // of this lane's box in the next tile to be issued
         int in_page = 0;
         int t0 = 0;      // that tile's first token
+        bool need = false;  // a token of that box counts
         auto fetch_page = [&]() {
             t0 = (pos.i < pos.s.a ? pos.i : pos.i + pos.s.f - pos.s.a) * C::TT;
             const int t = t0 + sub * box;
             const int entry = (int)(__umulhi((unsigned)t, p.page_mul) >> p.page_shift);
             in_page = t - entry * p.page_size;
-            if (t < pos.s.len) page = __ldg(p.table + (long long)pos.b * p.max_pages + entry);
+            need = t < pos.s.len &&
+                   ((p.S | p.W) == 0 || t < p.S || t + box > pos.s.len - p.W);
+            if (need) page = __ldg(p.table + (long long)pos.b * p.max_pages + entry);
         };
         bool first = true;
         auto issue = [&](int slot) {
             const int tokens = pos.s.len - t0;  // from here on
             const int h = p.blocks == 1 ? pos.u : pos.u / p.blocks;
             unsigned char* stage = ring + slot * C::STAGEB;
-            const int boxes = tokens >= C::TT ? down : (tokens + box - 1) / box;
-            if (sub < boxes && (unsigned)page >= (unsigned)p.n_pages) {
+            // Boxes outside the set are left out, their pages not looked at: a
+            // cache may have given them back.
+            const unsigned boxes = __ballot_sync(0xffffffffu, need) & ((1u << down) - 1u);
+            if (need && (unsigned)page >= (unsigned)p.n_pages) {
                 atomicOr(p.ctr + kCtrError, kErrPage);
                 page = 0;
             }
@@ -1258,7 +1263,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             if (elect_one()) {
                 meta[slot] = make_int4(pos.b, pos.u, pos.i, t0);
                 mbar_arrive_expect_tx(full + slot,
-                                      (uint32_t)(boxes * box * 2 * C::RB + rows * 2 * D));
+                                      (uint32_t)(__popc(boxes) * box * 2 * C::RB + rows * 2 * D));
             }
             if constexpr (C::kCopyQ) {
                 __syncwarp();
@@ -1268,7 +1273,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                                   (long long)(h * p.group + blk + lane) * D,
                               2 * D, full + slot, pol);
             }
-            for (int i = 0; i < boxes; ++i) {
+            for (unsigned some = boxes; some; some &= some - 1u) {
+                const int i = __ffs(some) - 1;
                 const int pg = __shfl_sync(0xffffffffu, page, i);
                 const int in = __shfl_sync(0xffffffffu, in_page, i);
                 unsigned char* dst = stage + i * (box * C::RB);
@@ -1281,7 +1287,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
                 // Lane = token: its scales, and its arrival once they landed.
                 const int pg = __shfl_sync(0xffffffffu, page, from);
                 const int in = __shfl_sync(0xffffffffu, in_page, from) + rem;
-                if (lane < tokens) {
+                if (lane < tokens && (boxes >> from & 1u)) {
                     const long long at = ((long long)pg * p.hkv + h) * p.page_size + in;
                     cp_async_4(scales + slot * 2 * C::TT + lane, p.ks + at);
                     cp_async_4(scales + slot * 2 * C::TT + C::TT + lane, p.vs + at);

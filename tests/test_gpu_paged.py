@@ -545,3 +545,25 @@ def test_shared_pages(cuda_device):
     check_attention(got, lse, attention(q, c["k64"], c["v64"], [160, 64]), [160, 64], 64, "bf16", F32)
 
 
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("f32", 128)])
+@pytest.mark.parametrize("page", [8, 16, 24, 64])
+@pytest.mark.parametrize("n_sink,window", [(4, 20), (0, 1), (40, 0), (1, 64), (33, 31)])
+def test_sink_set_of_a_cache_that_has_freed_the_rest(cuda_device, dtype, d, page, n_sink, window):
+    """Table entries without a token of the sink set are not looked at: a
+    sequence may have given those pages back."""
+    from paged_reference import attended
+    lens = [700, 65, 24, 1, 0, 333, 96, 1000]
+    c = make_cache(dtype, lens, page, 2, d, token_major=page == 24, seed=page + window)
+    table = torch.full_like(c["table"], -1)
+    for b, n in enumerate(lens):
+        kept = attended(n, n_sink, window).div(page, rounding_mode="floor").unique().cuda()
+        table[b, kept] = c["table"][b, kept]
+    assert bool((table != c["table"]).any())
+    c["table"] = table
+    for out in (F32, BF16):
+        # (Also checks that the error word is clear.)
+        _, q, _, got, lse = _decode(c, lens, 6, d, out, n_sink, window, seed=page, dtype=dtype)
+        ref = attention(q, c["k64"], c["v64"], lens, n_sink, window)
+        check_attention(got, lse, ref, lens, d, dtype, out)
