@@ -13,11 +13,30 @@ one new token per sequence over its pages (``PagedDecoder``) and a linear
 layer with its epilogue (``Linear``).
 
 The C ABI is include/alspec.h (libalspec.so); ``alspec`` is its ctypes
-binding.  Importing the package raises if libalspec.so is missing.
+binding.  Importing the package raises if libalspec.so is missing.  torch is
+imported where its tensors are taken, not with the package: the binding needs
+none.
 """
+from importlib import import_module as _import_module
+
 from .alspec import *  # noqa: F401,F403
 from .alspec import Decoder, AlspecError, make_desc, SIGNATURES, LIB_PATH  # noqa: F401
-from .linear import Linear  # noqa: F401
-from .paged import PagedCache, PagedDecoder  # noqa: F401
 
 __version__ = "0.1.0"
+
+# What takes torch tensors, and its module.
+_TENSOR_LAYER = {"Linear": ".linear", "PagedCache": ".paged", "PagedDecoder": ".paged",
+                 "linear": ".linear", "paged": ".paged"}
+
+
+def __getattr__(name):
+    if name not in _TENSOR_LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = _import_module(_TENSOR_LAYER[name], __name__)
+    value = module if name.islower() else getattr(module, name)
+    globals()[name] = value  # found there from now on
+    return value
+
+
+def __dir__():
+    return sorted({*globals(), *_TENSOR_LAYER})

@@ -22,9 +22,10 @@ _FLOATS = (torch.float32, torch.bfloat16)
 
 # The raw handle of the current stream; torch.cuda.current_stream builds an
 # object around it, which took longer (2.2 us) than the checks and the launch
-# of a small call.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# of a small call.  (A build of torch without CUDA has neither name, nor
+# tensors that would get as far.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _device(device):

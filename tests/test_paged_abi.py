@@ -5,6 +5,7 @@ import math
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -190,3 +191,54 @@ def test_c_sees_the_same_cache_description(tmp_path):
                                           check=True).stdout.split()]
     assert got == [ctypes.sizeof(ab.alspec_paged_cache), ab.alspec_paged_cache.page_stride.offset,
                    ab.alspec_paged_cache.dtype.offset]
+
+
+_BLOCKED = """
+import sys
+sys.modules["torch"] = None          # as where torch is not installed
+import speculative_flash_decoding_b200 as sfd
+c = sfd.alspec_paged_cache(n_pages=10, page_size=16, n_kv_heads=4, head_dim=128, dtype=sfd.ALSPEC_BF16)
+assert sfd.alspec_paged_workspace_size(c, 3, 8) > 0
+for name in ("PagedCache", "PagedDecoder", "Linear"):
+    assert name in dir(sfd)
+    try:
+        getattr(sfd, name)
+    except ImportError:
+        pass
+    else:
+        raise SystemExit(name)
+"""
+
+_CPU_TORCH = """
+import sys, torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)      # as in a build of torch without CUDA
+import speculative_flash_decoding_b200 as sfd
+assert sfd.Linear is sfd.linear.Linear and sfd.PagedCache is sfd.paged.PagedCache
+try:
+    sfd.PagedCache.from_tensors(torch.zeros(4, 2, 16, 64), torch.zeros(4, 2, 16, 64))
+except ValueError:
+    pass
+"""
+
+_LATE = """
+import sys
+import speculative_flash_decoding_b200 as sfd
+assert "torch" not in sys.modules
+from speculative_flash_decoding_b200 import Linear, PagedCache, PagedDecoder
+assert "torch" in sys.modules and sfd.PagedDecoder is PagedDecoder
+"""
+
+
+@pytest.mark.parametrize("code", [_BLOCKED, _CPU_TORCH, _LATE], ids=["no torch", "cpu torch", "late"])
+def test_the_binding_loads_without_torch(code):
+    """torch is needed where its tensors are: the ctypes binding takes plain
+    addresses."""
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+
+
+def test_unknown_names_are_refused():
+    with pytest.raises(AttributeError, match="no attribute 'Lineal'"):
+        sfd.Lineal
