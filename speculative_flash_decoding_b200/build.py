@@ -22,8 +22,9 @@ DEBUG_LIB = os.path.join(PKG, "libalspec_debug.so")
 PROBE_LIB = os.path.join(PKG, "libalspec_read_probe.so")
 _DECODE_SRCS = [os.path.join(CSRC, f) for f in ("alspec.cu", "linear.cu", "paged.cu")]
 _DECODE_DEPS = ([os.path.join(CSRC, f) for f in ("attn_kernels.cuh", "common.cuh", "host.h",
-                                                 "linear_kernels.cuh", "oproj_kernels.cuh",
-                                                 "paged_kernels.cuh", "ptx.cuh")] +
+                                                 "linear_kernels.cuh", "linear_plan.h",
+                                                 "oproj_kernels.cuh", "paged_kernels.cuh",
+                                                 "ptx.cuh")] +
                 [os.path.join(INCLUDE, "alspec.h")])
 # (library, its sources, the headers they depend on, extra nvcc flags)
 TARGETS = [

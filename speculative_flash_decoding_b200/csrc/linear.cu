@@ -11,6 +11,7 @@
 #include "alspec.h"
 #include "host.h"
 #include "linear_kernels.cuh"
+#include "linear_plan.h"
 
 namespace alspec {
 namespace {
@@ -41,19 +42,19 @@ alspec_status encode_matrix(CUtensorMap* whole, CUtensorMap* end, const void* ba
     return ALSPEC_OK;
 }
 
-// Clusters of `c` CTAs of the kernel that the current device holds at once
-// (asked once).
-int g_clusters[kMaxDevices][kLinMaxSplit + 1] = {};
+// Clusters of the kernel that the current device holds at once (asked once).
+LinClusters g_clusters[kMaxDevices] = {};
+bool g_clusters_known[kMaxDevices] = {};
 std::mutex g_clusters_mutex;
 
-bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
+bool resident_clusters(LinClusters* out) {
     int dev = 0;
     if (!ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return false;
     if (smem_attr_once(reinterpret_cast<const void*>(linear_kernel<false>), kLinSmem) != ALSPEC_OK)
         return false;
     std::lock_guard<std::mutex> lock(g_clusters_mutex);
-    int(&n)[kLinMaxSplit + 1] = g_clusters[dev];
-    for (int c = 1; c <= kLinMaxSplit && n[kLinMaxSplit] == 0; ++c) {
+    LinClusters& fit = g_clusters[dev];
+    for (int c = 1; c <= kLinMaxSplit && !g_clusters_known[dev]; ++c) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)c);
         cfg.blockDim = dim3(kLinThreads);
@@ -65,33 +66,15 @@ bool resident_clusters(int (&out)[kLinMaxSplit + 1]) {
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (!ok(cudaOccupancyMaxActiveClusters(&n[c], linear_kernel<false>, &cfg)) || n[c] < 1) {
-            n[kLinMaxSplit] = 0;
-            return false;
+        // A size that does not fit is no error: it is not chosen.
+        if (cudaOccupancyMaxActiveClusters(&fit.n[c], linear_kernel<false>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            fit.n[c] = 0;
         }
     }
-    for (int c = 0; c <= kLinMaxSplit; ++c) out[c] = n[c];
+    g_clusters_known[dev] = true;
+    *out = fit;
     return true;
-}
-
-// CTAs that share the K of a tile: the number that makes (waves of clusters)
-// x (blocks of a CTA, plus 16 for a wave's beginning and end and four for the
-// exchange where there is one) smallest.  Clusters leave SMs idle (148 SMs
-// hold 74 pairs, but 45 clusters of 3, 33 of 4, 26 of 5, 15 of 8), and a
-// second wave costs more than idle SMs: 33 x 4096 x 6144 (48 tiles) takes 24
-// us with 3, 19.6 with 5 and 15 with 2.
-// `ctas`: CTAs that work on a tile's block of K together.
-int choose_split(int64_t tiles, int kblocks, int ctas) {
-    int n[kLinMaxSplit + 1];
-    if (!resident_clusters(n)) return 0;
-    int best = 1;
-    int64_t least = INT64_MAX;
-    for (int c = 1; c * ctas <= kLinMaxSplit && c <= std::max(1, kblocks / 4); ++c) {
-        const int64_t waves = (tiles + n[c * ctas] - 1) / n[c * ctas];
-        const int64_t cost = waves * ((kblocks + c - 1) / c + (c > 1 ? 20 : 16));
-        if (cost < least) least = cost, best = c;
-    }
-    return best;
 }
 
 }  // namespace
@@ -124,9 +107,9 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     p.row_tiles = (int)(((int64_t)rows + most - 1) / most);
     p.nt = (int)((((int64_t)rows + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16);
     p.row_tiles = (rows - 1) / p.nt + 1;
-    // Large batches: pairs of CTAs, so that each brings half of x.  From 250
-    // rows on x is more bytes than W: 250 x 8192 x 8192 took 43.6 us without.
-    const bool pair = p.nt > kLinPair && n > kLinM;
+    LinClusters fit{};
+    if (!resident_clusters(&fit)) return ALSPEC_ERR_CUDA;
+    const bool pair = lin_pairs(fit, p.nt, n);
     if (pair) {
         p.nt = (p.nt + 31) / 32 * 32;
         p.row_tiles = (rows - 1) / p.nt + 1;
@@ -135,8 +118,7 @@ extern "C" alspec_status alspec_linear(const void* x, int64_t x_stride, const vo
     const int64_t tiles = ((int64_t)n + ctas * kLinM - 1) / (ctas * kLinM) * p.row_tiles;
     p.kblocks = (k - 1) / kLinK + 1;
     p.whole = k / kLinK;
-    p.split = choose_split(tiles, p.kblocks, ctas);
-    if (p.split == 0) return ALSPEC_ERR_CUDA;
+    p.split = lin_split(fit, tiles, p.kblocks, ctas);
     if (tiles * p.split * ctas > 0x7fffffff || n > 0x7fffffff - kLinM) return ALSPEC_ERR_UNSUPPORTED;
     // Blocks of a stage: four (512 consecutive bytes of a row of W) where the
     // ring holds two such stages, else two.  DRAM wants neighbouring columns

@@ -20,18 +20,16 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "linear_plan.h"
 #include "ptx.cuh"
 
 namespace alspec {
 
 constexpr int kLinThreads = 256;
-constexpr int kLinM = 128;        // features per tile
 constexpr int kLinK = 64;         // columns of a stage: 128 bytes
 constexpr int kLinMaxN = 256;     // batch rows per tile
 constexpr int kLinMaxStages = 12;
 constexpr int kLinSmem = 224 * 1024;  // dynamic shared memory, at most
-constexpr int kLinMaxSplit = 8;   // CTAs of a cluster
-constexpr int kLinPair = 128;     // batch rows of a tile up to which a CTA works alone
 constexpr int kLinPush = 48;      // batch rows of a small batch's tile, at most
 constexpr int kLinAhead = 8;      // blocks asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM

@@ -242,3 +242,52 @@ def test_the_binding_loads_without_torch(code):
 def test_unknown_names_are_refused():
     with pytest.raises(AttributeError, match="no attribute 'Lineal'"):
         sfd.Lineal
+
+
+_PLAN = r'''
+#include <cstdio>
+#include <cstdlib>
+#include "linear_plan.h"
+// argv: clusters of 1 .. 8 CTAs that fit; then per line of stdin: tiles kblocks ctas
+int main(int argc, char** argv) {
+    alspec::LinClusters fit{};
+    for (int c = 1; c <= 8; ++c) fit.n[c] = std::atoi(argv[c]);
+    std::printf("%d %d %d\n", alspec::lin_pairs(fit, 160, 1000), alspec::lin_pairs(fit, 128, 1000),
+                alspec::lin_pairs(fit, 160, 128));
+    long long tiles;
+    int kblocks, ctas;
+    while (std::scanf("%lld %d %d", &tiles, &kblocks, &ctas) == 3)
+        std::printf("%d\n", alspec::lin_split(fit, tiles, kblocks, ctas));
+}
+'''
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not installed")
+@pytest.mark.parametrize("fit", [
+    [148, 74, 45, 33, 26, 22, 17, 15],   # a whole device
+    [28, 14, 8, 7, 4, 3, 2, 0],          # parts without eight SMs together
+    [14, 7, 3, 2, 0, 0, 0, 0],
+    [5, 0, 0, 0, 0, 0, 0, 0],            # no pairs either
+    [0, 0, 0, 0, 0, 0, 0, 0],            # nothing known
+])
+def test_linear_takes_the_cluster_sizes_that_fit(tmp_path, fit):
+    src, exe = tmp_path / "plan.cpp", tmp_path / "plan"
+    src.write_text(_PLAN)
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I",
+                    os.path.join(ROOT, "speculative_flash_decoding_b200", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+    asked = [(t, kb, c) for t in (1, 3, 32, 48, 64, 400, 1 << 33) for kb in (1, 7, 8, 64, 128)
+             for c in (1, 2) if fit[c - 1] > 0 or c == 1]
+    out = subprocess.run([str(exe), *map(str, fit)], capture_output=True, text=True, check=True,
+                         input="".join("%d %d %d\n" % a for a in asked)).stdout.split()
+    assert [int(x) for x in out[:3]] == [int(fit[1] > 0), 0, 0]
+    for (tiles, kb, ctas), got in zip(asked, map(int, out[3:]), strict=True):
+        size = got * ctas
+        assert 1 <= size <= 8 and (size == 1 or fit[size - 1] > 0)
+
+        def cost(c):
+            return -(-tiles // max(1, fit[c * ctas - 1])) * (-(-kb // c) + (20 if c > 1 else 16))
+
+        able = [c for c in range(1, 9 // ctas + 1) if c * ctas <= 8 and c <= max(1, kb // 4)
+                and (c * ctas == 1 or fit[c * ctas - 1] > 0)]
+        assert cost(got) == min(map(cost, able))
