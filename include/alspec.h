@@ -252,7 +252,8 @@ alspec_status alspec_decode_traced(const alspec_desc* desc,
  * copies, two CTAs per SM).  The launch is programmatic: without `skip`, w
  * starts streaming before the kernel ahead of it on `stream` has completed
  * (x is read, and y written, only after it has), so w must not be written
- * by that kernel; with `skip`, nothing is read before it has completed.
+ * by that kernel (those further ahead may write it: they have completed);
+ * with `skip`, nothing is read before it has completed.
  *   x     device fp32 [batch][k], 16-byte aligned
  *   w     device bf16 [n][k] (row j = output feature j), 16-byte aligned
  *   y     device fp32 [batch][n]

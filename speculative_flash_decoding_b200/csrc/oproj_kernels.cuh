@@ -182,9 +182,6 @@ __global__ void __launch_bounds__(kObThreads, kObMinBlocks) oproj_bulk_kernel(co
     volatile int* abort = reinterpret_cast<volatile int*>(ticket + kObStages);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    // The kernel after this one on the stream may launch now (launched for
-    // that, it waits for this grid before it uses what this one writes).
-    pdl_launch_dependents();
     // x, the gate and y belong to the kernels ahead of this one, which may
     // still run (programmatic launch): the gate is read once they are done,
     // and nothing streams before it says there is work.  Without a gate
@@ -193,6 +190,7 @@ __global__ void __launch_bounds__(kObThreads, kObMinBlocks) oproj_bulk_kernel(co
     unsigned live = (1u << p.B) - 1u;
     if (p.skip) {
         pdl_wait_prerequisite();
+        pdl_launch_dependents();
         live = 0;
         for (int b = 0; b < p.B; ++b)
             if (p.skip[b] == 0) live |= 1u << b;
@@ -256,7 +254,14 @@ __global__ void __launch_bounds__(kObThreads, kObMinBlocks) oproj_bulk_kernel(co
     }
 
     // Consumers.
-    if (!p.skip) pdl_wait_prerequisite();
+    if (!p.skip) {
+        pdl_wait_prerequisite();
+        // Only now may the kernel after this one start (launched for that, it
+        // waits for this grid before it uses what this one writes): it may
+        // stream its own weights at once, as this one does, and a kernel
+        // ahead that let this one start early may be what writes them.
+        pdl_launch_dependents();
+    }
     for (int rl = warp; rl < nrows; rl += kObConsumers) {
         float2 acc[NB];
 #pragma unroll

@@ -215,3 +215,42 @@ def test_projection_behind_the_merge_reads_fresh_outputs(cuda_device):
                 assert _row_rel(y.cpu().numpy(), oracle.oproj(x, w_bits)).max() < ROW_TOL
         assert sfd.alspec_graph_destroy(g) == 0
     assert dec.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_oproj_behind_another_that_started_early(cuda_device, captured):
+    """A linear layer writes W, a projection of few rows with other weights
+    starts beside it, and a projection with W follows: W streams before the
+    kernel ahead has completed, but not before the linear layer has."""
+    import speculative_flash_decoding_b200 as sfd
+    rows, k, n = 512, 4096, 4096
+    g = torch.Generator(device="cpu").manual_seed(1)
+    xs = (torch.randn(3, rows, k, generator=g)).to(torch.bfloat16).to(cuda_device)
+    make = sfd.Linear(_bf16_weights(n, k, 2, cuda_device))
+    few, x = _bf16_weights(8, n, 3, cuda_device), torch.randn(1, n, generator=g).to(cuda_device)
+    w = torch.zeros(rows, n, dtype=torch.bfloat16, device=cuda_device)
+    y0, y = torch.empty(1, 8, device=cuda_device), torch.empty(1, rows, device=cuda_device)
+    src = xs[0].clone()
+    wants = []
+    for i in range(3):
+        made = make.apply(xs[i])
+        wants.append((x.double() @ made.double().t()).cpu().numpy())
+
+    def chain():
+        s = torch.cuda.current_stream().cuda_stream
+        make.apply(src, out=w)
+        for a, b, m in ((few, y0, 8), (w, y, rows)):
+            assert sfd.alspec_oproj(x.data_ptr(), a.data_ptr(), b.data_ptr(), 0, 1, n, m, s) == 0
+
+    graph = None
+    if captured:
+        chain()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain()
+    for trial in range(12):
+        src.copy_(xs[trial % 3])
+        w.zero_()
+        graph.replay() if captured else chain()
+        torch.cuda.synchronize()
+        assert _row_rel(y.cpu().numpy(), wants[trial % 3]).max() < ROW_TOL, trial
