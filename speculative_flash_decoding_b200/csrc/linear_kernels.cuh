@@ -177,8 +177,10 @@ __device__ __forceinline__ void lin_sum16(const LinearParams& p, uint32_t addr, 
 }
 
 // The activation of N sums: one branch on its kind, not one per sum.  SiLU
-// takes the fast exponential and quotient (a few units of 2^-23 of the
-// result, times |x| where it is far below zero).
+// takes the fast exponential, of x / 2 so that its square, and the quotient by
+// a number in [1, 2], stay in range wherever the result does: within 2^-20 +
+// |x| 2^-23 of the result.  (x over 1 + exp(-x) by the fast quotient is 0 from
+// -87.4 down, where the result is a normal number until -92.)
 template <int N>
 __device__ __forceinline__ void lin_activate(float (&x)[N], int act) {
     if (act == 1) {
@@ -189,7 +191,10 @@ __device__ __forceinline__ void lin_activate(float (&x)[N], int act) {
         for (int i = 0; i < N; ++i) x[i] = 0.5f * x[i] * (1.f + erff(x[i] * 0.70710678118654752f));
     } else if (act == 3) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = __fdividef(x[i], 1.f + __expf(-x[i]));
+        for (int i = 0; i < N; ++i) {
+            const float t = __expf(-0.5f * fabsf(x[i]));
+            x[i] = __fdividef(x[i] < 0.f ? x[i] * t * t : x[i], 1.f + t * t);
+        }
     }
 }
 

@@ -159,3 +159,31 @@ def test_captured_and_on_two_streams(cuda_device):
     torch.cuda.synchronize()
     for o in ys:
         assert torch.equal(o, y)
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_silu_keeps_its_relative_error_far_below_zero(cuda_device, rows):
+    """Every result that fp32 holds as a normal number is within 2^-20 +
+    |x| 2^-23 of itself: an exponential of x / 2 is off by 2^-22 and by the
+    rounding of its argument, |x| 2^-25, its square by twice that, the quotient
+    by 2^-22.  What is below 2^-126 may be anything as small."""
+    from speculative_flash_decoding_b200 import Linear
+    at = torch.tensor([-87.0, -87.5, -88.0, -89.0, -90.0, -91.5, -92.0, -95.0, -110.0, -1e30,
+                       -60.0, -20.0, -3.0, -0.01, 0.0, 0.5, 7.0, 88.0, 90.0, 1e30, 1e-38, -1e-38,
+                       30.0, -30.0]).to(BF16)
+    w = torch.eye(len(at), device="cuda").to(BF16)
+    x = at.cuda().repeat(rows, 1)
+    y = Linear(w, activation="silu").apply(x, out_dtype=F32).double()
+    z = x.double()
+    want = z * torch.exp(-torch.nn.functional.softplus(-z))
+    bound = want.abs() * (2.0 ** -20 + z.abs().clamp(max=200.0) * 2.0 ** -23) + 2.0 ** -126
+    err = (y - want).abs()
+    assert bool((err <= bound).all()), (err / bound)[0].tolist()
+    # Infinities and NaN as the formula has them.
+    x = torch.tensor([[math.inf, 1.0], [-math.inf, 1.0], [math.nan, 1.0]]).to(BF16).cuda()
+    w = torch.zeros(2, 8, device="cuda", dtype=BF16)
+    w[0, 0] = 1
+    xs = torch.zeros(3, 8, device="cuda", dtype=BF16)
+    xs[:, 0] = x[:, 0]
+    y = Linear(w[:1].contiguous(), activation="silu").apply(xs, out_dtype=F32)[:, 0]
+    assert y[0] == math.inf and bool(y[1:].isnan().all())
