@@ -187,3 +187,27 @@ def test_silu_keeps_its_relative_error_far_below_zero(cuda_device, rows):
     xs[:, 0] = x[:, 0]
     y = Linear(w[:1].contiguous(), activation="silu").apply(xs, out_dtype=F32)[:, 0]
     assert y[0] == math.inf and bool(y[1:].isnan().all())
+
+
+@pytest.mark.parametrize("rows", [1, 16, 200])
+def test_long_sums_keep_fp32(cuda_device, rows):
+    """fp32 outputs over 8192 columns: their blocks go round several
+    accumulators (as many of a tile's batch rows as 512 TMEM columns hold, up
+    to eight), because each of a chain's steps of 16 columns cuts the running
+    sum off, by half of 2^-23 on the average, and that sum is two thirds of
+    its end on the average: the whole shrinks by steps * 2 / 3 * 2^-24 at the
+    most, and eight more roundings of 2^-24 join the parts.  (With one
+    accumulator it is off by 4e-6 at 16 rows and twice that at 200.)"""
+    from speculative_flash_decoding_b200 import Linear
+    k, n = 8192, 8192
+    x, w, _, _ = _inputs(rows, n, k, seed=3, bias=False)
+    tiles = -(-rows // 128)
+    nt = -(-math.ceil(rows / tiles) // 16) * 16  # batch rows of a tile
+    cols = 32
+    while cols < nt:
+        cols *= 2
+    steps = k // 16 // min(8, 512 // cols)
+    y = Linear(w).apply(x, out_dtype=F32).double()
+    want = x.double() @ w.double().t()
+    rel = float((y - want).norm() / want.norm())
+    assert rel <= (steps * 2 / 3 + 8) * 2.0 ** -24, (rel, steps)
