@@ -1240,7 +1240,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, BOX>::kThreads, 1) paged_decode
             const int entry = (int)(__umulhi((unsigned)t, p.page_mul) >> p.page_shift);
             in_page = t - entry * p.page_size;
             need = t < pos.s.len &&
-                   ((p.S | p.W) == 0 || t < p.S || t + box > pos.s.len - p.W);
+                   ((p.S | p.W) == 0 || t < p.S || min(t + box, pos.s.len) > pos.s.len - p.W);
             if (need) page = __ldg(p.table + (long long)pos.b * p.max_pages + entry);
         };
         bool first = true;

@@ -549,12 +549,12 @@ def test_shared_pages(cuda_device):
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("f32", 128)])
 @pytest.mark.parametrize("page", [8, 16, 24, 64])
-@pytest.mark.parametrize("n_sink,window", [(4, 20), (0, 1), (40, 0), (1, 64), (33, 31)])
+@pytest.mark.parametrize("n_sink,window", [(4, 20), (0, 1), (40, 0), (4, 0), (1, 64), (33, 31)])
 def test_sink_set_of_a_cache_that_has_freed_the_rest(cuda_device, dtype, d, page, n_sink, window):
     """Table entries without a token of the sink set are not looked at: a
     sequence may have given those pages back."""
     from paged_reference import attended
-    lens = [700, 65, 24, 1, 0, 333, 96, 1000]
+    lens = [700, 65, 24, 1, 0, 333, 96, 1000, 21, 30]
     c = make_cache(dtype, lens, page, 2, d, token_major=page == 24, seed=page + window)
     table = torch.full_like(c["table"], -1)
     for b, n in enumerate(lens):
