@@ -499,7 +499,9 @@ typedef struct {
  * infinity reads back as NaN.  A row named twice in one call ends up with
  * one of the values given for each of its elements, not necessarily of the
  * same token.  n_tokens 0 is a no-op.  Rows that no token names keep their
- * contents.  Asynchronous on `stream`, one launch.
+ * contents.  k and v must not overlap the pages.  n_tokens * n_kv_heads is
+ * limited to 2^30 (ALSPEC_ERR_UNSUPPORTED).  Asynchronous on `stream`, one
+ * launch.
  */
 alspec_status alspec_paged_append(const alspec_paged_cache* cache, const void* k, const void* v,
                                   int src_dtype, int64_t k_stride, int64_t v_stride,
@@ -513,12 +515,14 @@ alspec_status alspec_paged_append(const alspec_paged_cache* cache, const void* k
  *                 [batch][n_kv_heads][max_seq_len][head_dim], 16-byte aligned
  *   seq_lens      device int32 [batch], 0 <= L_b <= min(max_seq_len,
  *                 max_pages * page_size): rows [0, L_b) of sequence b are
- *                 written (values, rounded once to out_dtype), rows from L_b
- *                 on keep their contents.  A length out of range is clamped
+ *                 written (the fp32 value, for e4m3 pages the fp32 product of
+ *                 code and scale, rounded to out_dtype), rows from L_b on keep
+ *                 their contents.  A length out of range is clamped
  *                 and sets ALSPEC_DEVERR_SEQ_LEN.
  *   err           device uint32 or NULL.  Rows of a page out of range are not
  *                 written and set ALSPEC_DEVERR_PAGE.
- * Asynchronous on `stream`, one launch.
+ * The outputs must overlap neither each other nor the pages.  Asynchronous on
+ * `stream`, one launch.
  */
 alspec_status alspec_paged_gather(const alspec_paged_cache* cache, const int32_t* page_table,
                                   int max_pages, const int32_t* seq_lens, int batch,
@@ -556,7 +560,8 @@ size_t alspec_paged_workspace_size(const alspec_paged_cache* cache, int batch, i
  *   n_sink, window  both 0: the whole cache
  *   scale       softmax scale, finite; 0 stands for 1/sqrt(head_dim)
  *   out         device [batch][n_q_heads][head_dim], out_dtype (ALSPEC_F32 or
- *               ALSPEC_BF16), 16-byte aligned
+ *               ALSPEC_BF16), 16-byte aligned; out and lse must overlap no
+ *               input
  *   lse         device fp32 [batch][n_q_heads] or NULL: the natural logarithm
  *               of sum_t exp(scale * q . k_t), for joining the output with
  *               attention over other tokens
@@ -604,7 +609,7 @@ typedef enum {
  *   w         device bf16 [n][k] contiguous, 16-byte aligned
  *   bias      device bf16 [n], or NULL
  *   residual  device [rows][n] contiguous in y's type, or NULL; it may be y
- *             itself
+ *             itself, but must not overlap it otherwise
  *   y         device [rows][n] contiguous, out_dtype ALSPEC_F32 or ALSPEC_BF16,
  *             aligned to its element; must not overlap x or w
  *   err       device uint32 or NULL: ALSPEC_DEVERR_TIMEOUT is ORed in when one

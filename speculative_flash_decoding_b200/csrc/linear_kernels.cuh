@@ -30,7 +30,13 @@ constexpr int kLinK = 64;         // columns of a stage: 128 bytes
 constexpr int kLinMaxN = 256;     // batch rows per tile
 constexpr int kLinMaxStages = 12;
 constexpr int kLinSmem = 224 * 1024;  // dynamic shared memory, at most
-constexpr int kLinPush = 48;      // batch rows of a small batch's tile, at most
+// Batch rows of a tile up to which parts of the sums are pushed to the CTA that
+// finishes their rows, instead of read by it: one cluster barrier less, a
+// buffer of split * slice * 512 bytes beside the ring more.  k = n = 4096, pushed
+// against read: 9.9 and 10.9 us for 1 row, 9.7 and 10.5 for 32, 10.0 and 10.9
+// for 48, 11.0 and 11.3 for 64, from where the ring is the better use of the
+// room.
+constexpr int kLinPush = 48;
 constexpr int kLinAhead = 8;      // blocks asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM
 // holds one CTA and its TMEM allocation never waits for another's.

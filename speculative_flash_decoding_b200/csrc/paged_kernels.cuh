@@ -96,7 +96,12 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendCtas = 6;  // CTAs for each SM, at most
+// CTAs for each SM that a launch asks for, at most.  Registers let two (fp32 to
+// e4m3) to four (bf16 to bf16) be resident; the others take over as those end.
+// 16411 tokens of 8 heads of 128 elements, bf16 to e4m3, bf16 to bf16 and fp32
+// to fp32: 20.3, 25.4 and 54.0 us with six; 19.6, 28.6 and 54.8 with three;
+// 23.5, 26.4 and 53.3 with four.
+constexpr int kAppendCtas = 6;
 
 // Two quotients x / s correctly rounded, from r = 1 / s rounded: the remainder
 // of the product is exact, and one more step with it rounds right (P.
@@ -351,13 +356,16 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(
 //               so far (wexp): 22 bits, or 2^-36 of that largest;
 //   fp32 pages  tf32 with hi + lo of both operands (2^-21.4).
 // Bound by HBM bytes over bf16 pages (128K tokens of 8 KV heads: 84 us, 6.4
-// TB/s), by instructions over e4m3 pages (8 x 16K-64K tokens: 147 us, 5.3 TB/s;
-// a tile of 8 KB takes 128 conversions and 64 MMAs) and fp32 pages (4 x 20000
+// TB/s), by instructions over e4m3 pages (8 x 16K-64K tokens: 148-153 us,
+// 5.1-5.3 TB/s; a tile of 8 KB takes 128 conversions and 64 MMAs) and fp32 pages (4 x 20000
 // tokens of 128 elements: 122-124 us, 5.3 TB/s), by the reads before the first
 // tile and the joins after the last where the sequences are short (123 of
 // 1-900 tokens: 30 us for 17.6 us of bytes).
 
-constexpr int kHeadRows = 8;    // query heads per work unit
+// Query heads per work unit.  A KV head's further eights are units of their
+// own, each of which streams its keys and values again (4 x 30000 bf16 tokens of
+// 4 KV heads of 128 elements: 46.9 us with 8 query heads each, 82.2 with 16).
+constexpr int kHeadRows = 8;
 
 // Page types of the decode kernel.  Wide: for fp32 outputs (bf16 pages: P with
 // a third term; both: a tile's products summed apart).

@@ -37,8 +37,9 @@ class Linear:
     def apply(self, x, residual=None, out=None, out_dtype=torch.bfloat16, stream=None):
         """x bf16 [rows, k] (rows may be slices of wider ones); residual, if
         given, and out are contiguous [rows, n] tensors of one type (fp32 or
-        bf16; ``out_dtype`` where out is to be made) and may be the same
-        tensor.  Returns out; a new one belongs to the stream of the call."""
+        bf16) and may be the same tensor; out overlaps nothing else that is
+        read.  Returns out; a new one has the residual's type, without a
+        residual ``out_dtype``, and belongs to the stream of the call."""
         dev, n = self.device, self.n
         rows = x.shape[0]
         xt = x.stride()

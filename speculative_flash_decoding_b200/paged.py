@@ -257,8 +257,9 @@ class PagedDecoder:
         rows may be slices of wider ones) over sequence b's first
         seq_lens[b] tokens (0: zeros), or with n_sink + window > 0 over its
         sink set.  Fills out (fp32 or bf16; new: q's type) and, if given, lse
-        (fp32 [batch, n_q_heads], natural logarithm); returns out.  A new out
-        belongs to the stream of the call."""
+        (fp32 [batch, n_q_heads], natural logarithm), which overlap no input;
+        returns out.  A new out belongs to the stream of the call.  Pages
+        without a token attended to need no table entry."""
         c = self.cache
         dev, shape = c.device, self._shape
         qt = q.stride()
