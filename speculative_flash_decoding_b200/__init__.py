@@ -18,6 +18,7 @@ imported where its tensors are taken, not with the package: the binding needs
 none.
 """
 from importlib import import_module as _import_module
+from importlib.util import find_spec as _find_spec
 
 from .alspec import *  # noqa: F401,F403
 from .alspec import Decoder, AlspecError, make_desc, SIGNATURES, LIB_PATH  # noqa: F401
@@ -27,6 +28,11 @@ __version__ = "0.1.0"
 # What takes torch tensors, and its module.
 _TENSOR_LAYER = {"Linear": ".linear", "PagedCache": ".paged", "PagedDecoder": ".paged",
                  "linear": ".linear", "paged": ".paged"}
+
+# `import *` brings them where there is a torch.
+__all__ = [name for name in dir() if not name.startswith("_")]
+if _find_spec("torch"):
+    __all__ += _TENSOR_LAYER
 
 
 def __getattr__(name):

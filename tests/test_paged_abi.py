@@ -209,6 +209,18 @@ for name in ("PagedCache", "PagedDecoder", "Linear"):
         raise SystemExit(name)
 """
 
+_STAR = """
+from speculative_flash_decoding_b200 import *
+assert Linear and PagedCache and PagedDecoder and Decoder and alspec_linear and SIGNATURES
+"""
+
+_STAR_BLOCKED = """
+import sys
+sys.modules["torch"] = None
+from speculative_flash_decoding_b200 import *
+assert Decoder and alspec_linear and "Linear" not in globals()
+"""
+
 _CPU_TORCH = """
 import sys, torch
 for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
@@ -231,7 +243,8 @@ assert "torch" in sys.modules and sfd.PagedDecoder is PagedDecoder
 """
 
 
-@pytest.mark.parametrize("code", [_BLOCKED, _CPU_TORCH, _LATE], ids=["no torch", "cpu torch", "late"])
+@pytest.mark.parametrize("code", [_BLOCKED, _CPU_TORCH, _LATE, _STAR, _STAR_BLOCKED],
+                         ids=["no torch", "cpu torch", "late", "star", "star, no torch"])
 def test_the_binding_loads_without_torch(code):
     """torch is needed where its tensors are: the ctypes binding takes plain
     addresses."""
