@@ -34,8 +34,9 @@ constexpr int kLinSmem = 224 * 1024;  // dynamic shared memory, at most
 // finishes their rows, instead of read by it: one cluster barrier less, a
 // buffer of split * slice * 512 bytes beside the ring more.  k = n = 4096, pushed
 // against read: 9.9 and 10.9 us for 1 row, 9.7 and 10.5 for 32, 10.0 and 10.9
-// for 48, 11.0 and 11.3 for 64, from where the ring is the better use of the
-// room.
+// for 48.  At 64 rows it still gains where K is split (11.0 and 11.3; 12.5 and
+// 13.7 with k = 8192, n = 2048), but loses where it is hardly or not (27.9 and
+// 27.4 with k = n = 8192, 16.0 and 14.8 with k = 2048, n = 16384).
 constexpr int kLinPush = 48;
 constexpr int kLinAhead = 8;      // blocks asked for before the kernel ahead has ended
 // More than half of an SM's shared memory whatever the sizes, so that an SM
